@@ -12,6 +12,10 @@ loudly when the library is missing.
     o      = decode_step(q, k, v, beta, S)          # S updated in place
     alpha, lam = gate(k, beta)
 
+The operators that stand around the mixer in a block (``norm_fwd``,
+``conv_fwd``, ``scan_fwd``, their backward passes and one-token steps) are in
+``block.py`` and offered here too.
+
 The method ("Exact Flow Linear Attention: Exact Solution from Continuous-Time
 Dynamics", papernotes.org summary of arXiv 2512.12602, 关键设计 2):
 S_t = (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T, o_t = S_t^T q_t,
@@ -42,7 +46,11 @@ STATUS = {0: "EFLA_OK", 1: "EFLA_ERR_NULL", 2: "EFLA_ERR_SHAPE", 3: "EFLA_ERR_DT
 EXPORTS = ("efla_status_string", "efla_version", "efla_last_error", "efla_gate",
            "efla_chunk_fwd_workspace_size", "efla_chunk_fwd", "efla_decode_step",
            "efla_chunk_fwd_workspace_size_simt", "efla_chunk_fwd_noalloc", "efla_diag_wait_timeout",
-           "efla_state_affine", "efla_prefill_bwd_workspace_size", "efla_prefill_bwd")
+           "efla_state_affine", "efla_prefill_bwd_workspace_size", "efla_prefill_bwd",
+           "efla_norm_fwd", "efla_norm_bwd_workspace_size", "efla_norm_bwd",
+           "efla_conv_fwd", "efla_conv_bwd_workspace_size", "efla_conv_bwd", "efla_conv_step",
+           "efla_scan_fwd_workspace_size", "efla_scan_fwd", "efla_scan_bwd_workspace_size", "efla_scan_bwd",
+           "efla_scan_step")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _p, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -295,3 +303,6 @@ def prefill_bwd(q, k, v, beta, S0, dO, dSL=None, mode: str = "exact", workspace=
 def prefill_bwd_workspace_size(B: int, H: int, L: int, d: int) -> int:
     return int(_lib.efla_prefill_bwd_workspace_size(B, H, L, d, d))
 
+
+from .block import (conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, scan_bwd,  # noqa: E402
+                    scan_bwd_workspace_size, scan_fwd, scan_fwd_workspace_size, scan_step)

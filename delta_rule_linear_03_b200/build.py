@@ -1,8 +1,9 @@
 """Build the EFLA CUDA library in-tree: ``delta_rule_linear_03_b200/libefla.so``.
 
-Compiles ``csrc/efla_api.cu`` (which includes every kernel header) for
-sm_100a only, with the CUDA runtime linked statically so the library needs
-nothing but the driver at run time.  Rebuilds when any source under
+Compiles ``csrc/efla_api.cu`` (the mixer) and ``csrc/efla_block_api.cu`` (the
+operators around it), which between them include every kernel header, side by
+side for sm_100a only, and links them with the CUDA runtime, statically, so the
+library needs nothing but the driver at run time.  Rebuilds when any source under
 ``csrc/`` or ``include/`` is newer than the library.
 
     python delta_rule_linear_03_b200/build.py [--force]
@@ -23,8 +24,9 @@ SO = os.path.join(HERE, "libefla.so")
 SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu")) +
                  glob.glob(os.path.join(HERE, "csrc", "*.cuh")) +
                  glob.glob(os.path.join(ROOT, "include", "*.h")))
+UNITS = ("efla_api", "efla_block_api")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-              "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-Xptxas", "-v"]
+              "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 
 
 def nvcc() -> str:
@@ -45,13 +47,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return SO
     tmp = SO + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-o", tmp, os.path.join(HERE, "csrc", "efla_api.cu")]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libefla.so")
+    objs = [f"{tmp}.{u}.o" for u in UNITS]
+    try:
+        runs = [subprocess.Popen([nvcc(), *NVCC_FLAGS, "-c", "-o", o, os.path.join(HERE, "csrc", u + ".cu")],
+                                 stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                for u, o in zip(UNITS, objs)]
+        said = [r.communicate()[0] for r in runs]
+        for u, r, text in zip(UNITS, runs, said):
+            if r.returncode != 0:
+                sys.stderr.write(text)
+                raise RuntimeError(f"nvcc failed compiling {u}.cu")
+        r = subprocess.run([nvcc(), "-shared", "-cudart", "static", "-o", tmp, *objs], capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("nvcc failed linking libefla.so")
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     if verbose:
-        sys.stderr.write(r.stderr)
+        sys.stderr.write("".join(said))
     os.replace(tmp, SO)
     return SO
 

@@ -6,8 +6,6 @@
 #include <cstdint>
 #include <cstring>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/efla.h"
 #include "efla_backward.cuh"
 #include "efla_chunk_simt.cuh"
@@ -15,32 +13,12 @@
 #include "efla_common.cuh"
 #include "efla_decode.cuh"
 #include "efla_gate.cuh"
+#include "efla_host.cuh"
 
 using namespace efla;
+using namespace efla::host;
 
 namespace {
-
-constexpr long long kMaxElems = (1LL << 46);  // sanity bound on any tensor's element count
-
-// NVTX range around one C-ABI call (validation and launches), so a profiler
-// timeline shows which library call enqueued which kernels.  Header-only
-// NVTX: without an attached tool a push or pop is a test of a null pointer.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-size_t esize(efla_dtype_t dt) { return dt == EFLA_F32 ? 4 : 2; }
 
 efla_status_t check_common(efla_dtype_t dtype, efla_mode_t mode) {
     if (dtype != EFLA_F32 && dtype != EFLA_BF16) return EFLA_ERR_DTYPE;
@@ -53,18 +31,6 @@ efla_status_t check_head(int d_k, int d_v) {
     if (d_k != d_v) return EFLA_ERR_UNSUPPORTED;
     if (d_k != 32 && d_k != 64 && d_k != 128) return EFLA_ERR_UNSUPPORTED;
     return EFLA_OK;
-}
-
-efla_status_t launched() { return cudaGetLastError() == cudaSuccess ? EFLA_OK : EFLA_ERR_CUDA; }
-
-int num_sms() {
-    static std::atomic<int> cached[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    if ((n = cached[dev & 63].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cached[dev & 63].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 template <typename T, int D>

@@ -11,9 +11,9 @@ namespace efla {
 
 // Sticky device error word: a kernel whose bounded wait gives up ORs a
 // reason bit in here and returns; efla_last_error() reads and clears it.
-// The library is one translation unit (efla_api.cu includes every kernel
-// header), so the definition lives here.
-__device__ unsigned int g_error_word = 0u;
+// Every kernel with a bounded wait is compiled in efla_api.cu, which also
+// reads the word; another translation unit has a copy that nothing uses.
+static __device__ unsigned int g_error_word = 0u;
 
 enum : unsigned int { kErrTimeout = 1u };
 

@@ -1,0 +1,443 @@
+// efla_norm.cuh - root-mean-square norm of rows with the residual's addition
+// and an optional 8-bit output with scales, and its backward pass.
+//
+//   h = x + res,  rstd = 1 / sqrt(mean h^2 + eps),  y = h rstd w,  res_out = h
+//   8 bits: scale = max(max |y| / 448, 2^-126) over a group of 128 columns or
+//   the row, y8 = e4m3(y / scale)
+//   backward: u = w dy,  dh = rstd (u - h rstd^2 mean(u h)) + dres_out,
+//             dw = sum over rows of dy h rstd
+//
+// HBM bound: a handful of flops an element.  A row stays in registers
+// between the sum of its squares and its output, so each tensor crosses HBM
+// once.  TPR threads share a row with 16-byte accesses, IT of them each, and
+// RPI rows are in flight a thread; the row's sums go through shuffles and,
+// from 64 threads on, one exchange in shared memory for all RPI rows.  h is
+// the unrounded fp32 sum for the norm; res_out is its rounding.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "efla_vec.cuh"
+
+namespace efla {
+namespace norm {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: no scale is 0 or subnormal
+constexpr int kGroup = 128;
+constexpr int kMaxC = 16384;
+
+template <int TPR> constexpr int kThreadsOf = TPR > 256 ? TPR : 256;
+
+// Sums (or maxima of non-negative floats' bit patterns, which order as the
+// floats do and keep a NaN) of V values over the TPR threads of a row.
+template <int TPR, int V> struct RowReduce {
+    static constexpr int NW = kThreadsOf<TPR> / 32;
+    float red[TPR > 32 ? V : 1][TPR > 32 ? NW : 1];
+
+    __device__ __forceinline__ void sum(float (&v)[V]) {
+#pragma unroll
+        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if constexpr (TPR > 32) {
+            const int warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) red[i][warp] = v[i];
+            __syncthreads();
+            const int w0 = warp / (TPR / 32) * (TPR / 32);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < TPR / 32; ++k) s += red[i][w0 + k];
+                v[i] = s;
+            }
+        }
+    }
+    __device__ __forceinline__ void max_bits(uint32_t (&v)[V]) {
+#pragma unroll
+        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = max(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+        if constexpr (TPR > 32) {
+            const int warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) red[i][warp] = __uint_as_float(v[i]);
+            __syncthreads();
+            const int w0 = warp / (TPR / 32) * (TPR / 32);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < TPR / 32; ++k) v[i] = max(v[i], __float_as_uint(red[i][w0 + k]));
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// A group's scale from its largest |y|; a NaN stays one.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    const float a = __uint_as_float(bits) / kE4m3Max;
+    return a < kScaleMin ? kScaleMin : a;
+}
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+struct FwdArgs {
+    const void *x, *res;
+    const float *w;
+    void *y, *res_out;
+    unsigned char *y8;
+    float *scale;
+    float eps;
+    int group;  // columns of one scale: 128, or 0 for the row
+    int C;
+    long long rows;
+};
+
+// Rows whose width is a multiple of the 16-byte vector.
+template <typename T, typename R, int TPR, int IT, int RPI>
+__global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
+    constexpr int VEC = 16 / sizeof(T), SLOTS = kThreadsOf<TPR> / TPR;
+    constexpr int LPG = kGroup / VEC < TPR ? kGroup / VEC : TPR;  // lanes of one group of 128 columns
+    __shared__ RowReduce<TPR, RPI> rs, rm;
+    const int slot = threadIdx.x / TPR, l = threadIdx.x % TPR, C = a.C;
+    const long long row0 = (long long)blockIdx.x * (SLOTS * RPI) + slot;
+    const T *x = static_cast<const T *>(a.x);
+    const R *res = static_cast<const R *>(a.res);
+
+    Raw<T, VEC> xr[RPI][IT];
+    Raw<R, VEC> rr[RPI][IT];
+#pragma unroll
+    for (int i = 0; i < RPI; ++i)
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const long long row = row0 + i * SLOTS;
+            const int c = (k * TPR + l) * VEC;
+            const bool in = row < a.rows && c < C;
+            xr[i][k] = in ? load_raw<T, VEC>(x + row * C + c) : zero_raw<T, VEC>();
+            if (res) rr[i][k] = in ? load_raw<R, VEC>(res + row * C + c) : zero_raw<R, VEC>();
+        }
+    float h[RPI][IT][VEC], ss[RPI];
+#pragma unroll
+    for (int i = 0; i < RPI; ++i) {
+        ss[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            widen<T, VEC>(xr[i][k], h[i][k]);
+            if (res)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) h[i][k][j] += to_f32(rr[i][k].e[j]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) ss[i] = fmaf(h[i][k][j], h[i][k][j], ss[i]);
+        }
+    }
+    float w[IT][VEC];
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+        const int c = (k * TPR + l) * VEC;
+        widen<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
+    }
+    rs.sum(ss);
+    uint32_t top[RPI];
+#pragma unroll
+    for (int i = 0; i < RPI; ++i) {
+        const long long row = row0 + i * SLOTS;
+        const float rstd = 1.f / sqrtf(ss[i] / (float)C + a.eps);
+        top[i] = 0u;
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int c = (k * TPR + l) * VEC;
+            const bool in = row < a.rows && c < C;
+            if (a.res_out && in) store_raw<R, VEC>(static_cast<R *>(a.res_out) + row * C + c, narrow<R, VEC>(h[i][k]));
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                h[i][k][j] = in ? h[i][k][j] * rstd * w[k][j] : 0.f;  // columns past C: no part of a maximum
+                top[i] = max(top[i], abs_bits(h[i][k][j]));
+            }
+            if (a.y && in) store_raw<T, VEC>(static_cast<T *>(a.y) + row * C + c, narrow<T, VEC>(h[i][k]));
+        }
+    }
+    if (!a.y8) return;
+    if (!a.group) rm.max_bits(top);
+    const int ng = a.group ? (C + kGroup - 1) / kGroup : 1;
+#pragma unroll
+    for (int i = 0; i < RPI; ++i) {
+        const long long row = row0 + i * SLOTS;
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int c = (k * TPR + l) * VEC;
+            uint32_t m = top[i];
+            if (a.group) {
+                m = 0u;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) m = max(m, abs_bits(h[i][k][j]));
+#pragma unroll
+                for (int o = LPG / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
+            const float s = scale_of(m), inv = 1.f / s;
+            if (row >= a.rows || c >= C) continue;
+            if (a.group ? l % LPG == 0 : (l == 0 && k == 0)) a.scale[row * ng + (a.group ? c / kGroup : 0)] = s;
+            uint16_t q[VEC / 2];
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) q[j / 2] = e4m3x2(h[i][k][j] * inv, h[i][k][j + 1] * inv);
+            unsigned char *p = a.y8 + row * C + c;
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint2 *>(p) =
+                    make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+            else
+                *reinterpret_cast<uint32_t *>(p) = q[0] | (uint32_t)q[1] << 16;
+        }
+    }
+}
+
+// Any width: WPR warps share a row, each takes whole groups of 128 columns,
+// IT of them, four single elements a lane, so that a group's maximum stays
+// within one warp.
+template <typename T, typename R, int WPR, int IT>
+__global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_fwd_any_kernel(FwdArgs a) {
+    constexpr int TPR = WPR * 32, SLOTS = kThreadsOf<TPR> / TPR;
+    __shared__ RowReduce<TPR, 1> rs, rm;
+    const int slot = threadIdx.x / TPR, wr = threadIdx.x % TPR / 32, lane = threadIdx.x & 31, C = a.C;
+    const long long row = (long long)blockIdx.x * SLOTS + slot;
+    const bool on = row < a.rows;
+    const T *x = static_cast<const T *>(a.x) + row * C;
+    const R *res = a.res ? static_cast<const R *>(a.res) + row * C : nullptr;
+    float h[IT][4], ss[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+            h[k][j] = on && c < C ? to_f32(x[c]) : 0.f;
+            if (res && on && c < C) h[k][j] += to_f32(res[c]);
+        }
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ss[0] = fmaf(h[k][j], h[k][j], ss[0]);
+    rs.sum(ss);
+    const float rstd = 1.f / sqrtf(ss[0] / (float)C + a.eps);
+    uint32_t top[1] = {0u};
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+            if (!on || c >= C) {
+                h[k][j] = 0.f;
+                continue;
+            }
+            if (a.res_out) static_cast<R *>(a.res_out)[row * C + c] = from_f32<R>(h[k][j]);
+            h[k][j] = h[k][j] * rstd * a.w[c];
+            if (a.y) static_cast<T *>(a.y)[row * C + c] = from_f32<T>(h[k][j]);
+            top[0] = max(top[0], abs_bits(h[k][j]));
+        }
+    if (!a.y8) return;
+    if (!a.group) rm.max_bits(top);
+    const int ng = a.group ? (C + kGroup - 1) / kGroup : 1;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+        uint32_t m = top[0];
+        if (a.group) {
+            m = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max(m, abs_bits(h[k][j]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        const float s = scale_of(m), inv = 1.f / s;
+        const int g = k * WPR + wr;
+        if (!on || g * kGroup >= C) continue;
+        if (lane == 0 && (a.group || g == 0)) a.scale[row * ng + (a.group ? g : 0)] = s;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = g * kGroup + j * 32 + lane;
+            if (c < C) a.y8[row * C + c] = (unsigned char)(e4m3x2(h[k][j] * inv, 0.f) & 0xffu);
+        }
+    }
+}
+
+struct BwdArgs {
+    const void *dy, *h, *dres_out;
+    const float *w;
+    void *dx, *dres;  // dx in the type of dy, dres in the type of h; either may be NULL
+    float *part;      // [blocks][C]
+    float eps;
+    int C;
+    long long rows;
+};
+
+// A persistent block keeps its columns' share of dw in registers over all of
+// its rows; the shares of its row slots meet in shared memory at the end.
+template <typename T, typename R, int TPR, int IT, int RPI>
+__global__ void __launch_bounds__(kThreadsOf<TPR>) norm_bwd_kernel(BwdArgs a) {
+    constexpr int VEC = 16 / sizeof(T), NT = kThreadsOf<TPR>, SLOTS = NT / TPR;
+    __shared__ RowReduce<TPR, 2 * RPI> rs[2];
+    __shared__ float cols[SLOTS > 1 ? SLOTS : 1][SLOTS > 1 ? TPR * IT * VEC : 1];
+    const int slot = threadIdx.x / TPR, l = threadIdx.x % TPR, C = a.C;
+    const T *dy = static_cast<const T *>(a.dy);
+    const R *h = static_cast<const R *>(a.h), *dr = static_cast<const R *>(a.dres_out);
+    float w[IT][VEC], acc[IT][VEC];
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+        const int c = (k * TPR + l) * VEC;
+        widen<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[k][j] = 0.f;
+    }
+    int par = 0;
+    for (long long base = (long long)blockIdx.x * (SLOTS * RPI); base < a.rows;
+         base += (long long)gridDim.x * (SLOTS * RPI), par ^= 1) {
+        Raw<T, VEC> yr[RPI][IT];
+        Raw<R, VEC> hr[RPI][IT], rr[RPI][IT];
+#pragma unroll
+        for (int i = 0; i < RPI; ++i)
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const long long row = base + i * SLOTS + slot;
+                const int c = (k * TPR + l) * VEC;
+                const bool in = row < a.rows && c < C;
+                yr[i][k] = in ? load_raw<T, VEC>(dy + row * C + c) : zero_raw<T, VEC>();
+                hr[i][k] = in ? load_raw<R, VEC>(h + row * C + c) : zero_raw<R, VEC>();
+                rr[i][k] = in && dr ? load_raw<R, VEC>(dr + row * C + c) : zero_raw<R, VEC>();
+            }
+        float s[2 * RPI];  // sum h^2, sum u h
+#pragma unroll
+        for (int i = 0; i < RPI; ++i) {
+            s[2 * i] = s[2 * i + 1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float hv = to_f32(hr[i][k].e[j]);
+                    s[2 * i] = fmaf(hv, hv, s[2 * i]);
+                    s[2 * i + 1] = fmaf(to_f32(yr[i][k].e[j]) * w[k][j], hv, s[2 * i + 1]);
+                }
+        }
+        rs[par].sum(s);
+#pragma unroll
+        for (int i = 0; i < RPI; ++i) {
+            const long long row = base + i * SLOTS + slot;
+            const float rstd = 1.f / sqrtf(s[2 * i] / (float)C + a.eps);
+            const float m = rstd * rstd * (s[2 * i + 1] / (float)C);
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const int c = (k * TPR + l) * VEC;
+                if (row >= a.rows || c >= C) continue;
+                float d[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float hv = to_f32(hr[i][k].e[j]), yv = to_f32(yr[i][k].e[j]);
+                    acc[k][j] = fmaf(yv, hv * rstd, acc[k][j]);
+                    d[j] = fmaf(rstd, yv * w[k][j] - hv * m, to_f32(rr[i][k].e[j]));
+                }
+                if (a.dx) store_raw<T, VEC>(static_cast<T *>(a.dx) + row * C + c, narrow<T, VEC>(d));
+                if (a.dres) store_raw<R, VEC>(static_cast<R *>(a.dres) + row * C + c, narrow<R, VEC>(d));
+            }
+        }
+    }
+    float *part = a.part + (long long)blockIdx.x * C;
+    if constexpr (SLOTS > 1) {
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) cols[slot][(k * TPR + l) * VEC + j] = acc[k][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += NT) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) t += cols[i][c];
+            part[c] = t;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int c = (k * TPR + l) * VEC;
+            if (c < C) store_raw<float, VEC>(part + c, narrow<float, VEC>(acc[k]));
+        }
+    }
+}
+
+// Any width, as norm_fwd_any_kernel lays rows out.
+template <typename T, typename R, int WPR, int IT>
+__global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdArgs a) {
+    constexpr int TPR = WPR * 32, NT = kThreadsOf<TPR>, SLOTS = NT / TPR;
+    __shared__ RowReduce<TPR, 2> rs[2];
+    __shared__ float cols[SLOTS > 1 ? SLOTS : 1][SLOTS > 1 ? WPR * IT * kGroup : 1];
+    const int slot = threadIdx.x / TPR, wr = threadIdx.x % TPR / 32, lane = threadIdx.x & 31, C = a.C;
+    const T *dy = static_cast<const T *>(a.dy);
+    const R *h = static_cast<const R *>(a.h), *dr = static_cast<const R *>(a.dres_out);
+    float w[IT][4], acc[IT][4];
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+            w[k][j] = c < C ? a.w[c] : 0.f;
+            acc[k][j] = 0.f;
+        }
+    int par = 0;
+    for (long long base = (long long)blockIdx.x * SLOTS; base < a.rows; base += (long long)gridDim.x * SLOTS, par ^= 1) {
+        const long long row = base + slot;
+        const bool on = row < a.rows;
+        float hv[IT][4], yv[IT][4], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+                const bool in = on && c < C;
+                hv[k][j] = in ? to_f32(h[row * C + c]) : 0.f;
+                yv[k][j] = in ? to_f32(dy[row * C + c]) : 0.f;
+            }
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[0] = fmaf(hv[k][j], hv[k][j], s[0]);
+                s[1] = fmaf(yv[k][j] * w[k][j], hv[k][j], s[1]);
+            }
+        rs[par].sum(s);
+        const float rstd = 1.f / sqrtf(s[0] / (float)C + a.eps);
+        const float m = rstd * rstd * (s[1] / (float)C);
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+                if (!on || c >= C) continue;
+                acc[k][j] = fmaf(yv[k][j], hv[k][j] * rstd, acc[k][j]);
+                const float d = fmaf(rstd, yv[k][j] * w[k][j] - hv[k][j] * m, dr ? to_f32(dr[row * C + c]) : 0.f);
+                if (a.dx) static_cast<T *>(a.dx)[row * C + c] = from_f32<T>(d);
+                if (a.dres) static_cast<R *>(a.dres)[row * C + c] = from_f32<R>(d);
+            }
+    }
+    float *part = a.part + (long long)blockIdx.x * C;
+    if constexpr (SLOTS > 1) {
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cols[slot][(k * WPR + wr) * kGroup + j * 32 + lane] = acc[k][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += NT) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) t += cols[i][c];
+            part[c] = t;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+                if (c < C) part[c] = acc[k][j];
+            }
+    }
+}
+
+}  // namespace norm
+}  // namespace efla

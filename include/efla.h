@@ -245,6 +245,138 @@ efla_status_t efla_chunk_fwd_noalloc(const void *q, const void *k, const void *v
                                      int B, int H, int L, int d_k, int d_v,
                                      efla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the mixer.  A block has the norm of the residual
+ * stream in front of its projections, the short convolution on what they
+ * give (the pages' layer has one of width 4, jsqmd.com blog 4.1), the mixer
+ * (or, in layers that mix the two, a selective state space scan), and the
+ * norm of the mixer's output per head.  The pages print no formulas for
+ * these; they are the usual ones, written below.
+ *
+ * Conventions beyond those above: activations are [B][L][channels]
+ * (channels-last) in `dtype`; parameters and recurrent states are fp32,
+ * except the convolution's state, which is the last inputs themselves and has
+ * their dtype.  Where a call takes a row stride (ld...), in elements, token
+ * (b, t) is at base + (b * L + t) * ld, so a column slice of a wider
+ * projection can be passed as it is; such a base needs the alignment of its
+ * element alone (16-byte aligned rows of whole vectors are faster).  All
+ * other pointers are 16-byte aligned and dense.  `lengths` [B] (int32,
+ * device; NULL: all L) is each sequence's number of tokens, taken into
+ * [0, L]: tokens from there on are padding, which is not read into any
+ * result; their outputs and gradients are zeros.  Outputs must not overlap
+ * inputs or each other, except where a call says so.  Gradients of
+ * activations have the activations' dtype, gradients of parameters are fp32.
+ * Every sum is taken in fp32 in a fixed order: the same call gives the same
+ * bits.
+ */
+
+/*
+ * efla_norm_fwd - root-mean-square norm of rows, with the residual's addition:
+ *     h = x + res,  y = h / sqrt(mean(h^2) + eps) * weight,  res_out = h
+ *   x [rows][C] dtype `dtype`; res, res_out [rows][C] dtype `res_dtype` (the
+ *   dtype of x, or fp32), or both NULL; res_out may be NULL
+ *   weight [C] fp32
+ *   y [rows][C] dtype `dtype`, or NULL
+ *   y8 [rows][C] e4m3, scale [rows][ceil(C / group)] fp32, or both NULL:
+ *     scale = max(max |y| / 448, 2^-126) over each group of columns,
+ *     y8 = y / scale rounded to e4m3 (y from the fp32 value, not its rounding)
+ *   group: 128, or 0 for one scale a row.  C <= 16384.
+ * At least one of y and y8.  In place: res_out may be res; y or res_out may
+ * be x (res_out only where the dtypes agree).
+ */
+efla_status_t efla_norm_fwd(const void *x, efla_dtype_t dtype, const void *res, efla_dtype_t res_dtype,
+                            const float *weight, float eps, void *y, void *y8, float *scale, int group, void *res_out,
+                            long long rows, int C, efla_stream_t stream);
+
+/*
+ * efla_norm_bwd - its backward pass.  With h the sum that was normed
+ * (res_out, or x), dy the gradient of y and dres_out that of res_out (NULL: 0):
+ *     u = weight dy,  dh = (u - h mean(u h) / (mean(h^2) + eps)) / sqrt(mean(h^2) + eps) + dres_out
+ *     dweight = sum over rows of dy h / sqrt(mean(h^2) + eps)
+ *   dy [rows][C] `dtype`; h, dres_out [rows][C] `h_dtype` (the dtype of dy, or fp32)
+ *   dx [rows][C] `dtype` and dres [rows][C] `h_dtype` are dh; either may be NULL
+ *   dweight [C] fp32
+ */
+size_t efla_norm_bwd_workspace_size(long long rows, int C);
+efla_status_t efla_norm_bwd(const void *dy, efla_dtype_t dtype, const void *h, efla_dtype_t h_dtype,
+                            const float *weight, float eps, const void *dres_out, void *dx, void *dres, float *dweight,
+                            long long rows, int C, void *workspace, size_t workspace_bytes, efla_stream_t stream);
+
+/*
+ * efla_conv_fwd - short causal convolution along the sequence, a filter of
+ * K = 2, 3 or 4 taps a channel, with SiLU if `silu`:
+ *     y_t = act(bias + sum_j weight[j] x_{t-K+1+j}),  j = 0 .. K-1
+ *   x [B][L][C] rows `ldx` apart; weight [C][K], bias [C] (or NULL) fp32
+ *   state [B][K-1][C] `dtype`: the K-1 inputs before x, oldest first (NULL: 0)
+ *   state_out [B][K-1][C]: the last K-1 inputs of each sequence (or NULL); may be `state`
+ *   y: [B][L][C] where heads is 0, else [B][heads][L][C / heads], the layout
+ *     of the mixer's q, k and v
+ */
+efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, const float *weight, const float *bias,
+                            const void *state, const int *lengths, int silu, void *y, int heads, void *state_out,
+                            int B, int L, int C, int K, efla_stream_t stream);
+
+/*
+ * efla_conv_bwd - its backward pass.  dy has the layout of y; dstate_out is
+ * the gradient of state_out (NULL: 0).  dx [B][L][C] dense; dweight [C][K],
+ * dbias [C] (or NULL), dstate [B][K-1][C] `dtype` (or NULL).
+ */
+size_t efla_conv_bwd_workspace_size(int B, int L, int C, int K);
+efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_dtype_t dtype, const float *weight,
+                            const float *bias, const void *state, const int *lengths, int silu, int heads,
+                            const void *dstate_out, void *dx, float *dweight, float *dbias, void *dstate, int B, int L,
+                            int C, int K, void *workspace, size_t workspace_bytes, efla_stream_t stream);
+
+/*
+ * efla_conv_step - one token: x [B][C] rows `ldx` apart, state [B][K-1][C]
+ * updated in place, y [B][C].
+ */
+efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, void *state, const float *weight,
+                             const float *bias, int silu, void *y, int B, int C, int K, efla_stream_t stream);
+
+/*
+ * efla_scan_fwd - selective state space scan, N state values a channel:
+ *     D_t = softplus(dt_t + dt_bias)   (dt_t + dt_bias where `softplus` is 0)
+ *     h_t = exp(D_t A) h_{t-1} + D_t x_t B_t,   y_t = (<C_t, h_t> + D x_t) silu(z_t)
+ *   x, dt, z [B][L][C] rows ldx, lddt, ldz apart (z may be NULL: no gate)
+ *   Bm, Cm [B][L][G][N] tokens ldb, ldc apart; channel c reads group c / (C / G)
+ *   A [C][N] fp32, finite; D [C], dt_bias [C] fp32 (or NULL: 0)
+ *   h0 [B][C][N] fp32 (NULL: 0); h_L [B][C][N] fp32 (or NULL); h_L may be h0
+ *   y [B][L][C]
+ * N in {8, 16, 32, 64}; G divides C.
+ */
+size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N);
+efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
+                            const void *Bm, long long ldb, const void *Cm, long long ldc, const float *D, const void *z,
+                            long long ldz, const float *dt_bias, const float *h0, const int *lengths,
+                            efla_dtype_t dtype, int softplus, void *y, float *h_L, int B, int L, int C, int G, int N,
+                            void *workspace, size_t workspace_bytes, efla_stream_t stream);
+
+/*
+ * efla_scan_bwd - its backward pass, from dy [B][L][C] and dh_L [B][C][N]
+ * (NULL: 0): dx, ddt, dz [B][L][C] (dz where there is z), dB, dC
+ * [B][L][G][N], all dense in `dtype`; dA [C][N], dD [C] (or NULL), ddt_bias
+ * [C] (or NULL), dh0 [B][C][N] (or NULL) fp32.  Nothing of the forward pass
+ * is kept for it: the states are recomputed.
+ */
+size_t efla_scan_bwd_workspace_size(int B, int L, int C, int G, int N);
+efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const void *dt, long long lddt,
+                            const float *A, const void *Bm, long long ldb, const void *Cm, long long ldc,
+                            const float *D, const void *z, long long ldz, const float *dt_bias, const float *h0,
+                            const int *lengths, const float *dh_L, efla_dtype_t dtype, int softplus, void *dx,
+                            void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *dh0,
+                            int B, int L, int C, int G, int N, void *workspace, size_t workspace_bytes,
+                            efla_stream_t stream);
+
+/*
+ * efla_scan_step - one token: x, dt, z [B][C], Bm, Cm [B][G][N] (rows ld...
+ * apart), h [B][C][N] fp32 updated in place, y [B][C].  B <= 65535.
+ */
+efla_status_t efla_scan_step(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
+                             const void *Bm, long long ldb, const void *Cm, long long ldc, const float *D,
+                             const void *z, long long ldz, const float *dt_bias, efla_dtype_t dtype, int softplus,
+                             float *h, void *y, int B, int C, int G, int N, efla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
