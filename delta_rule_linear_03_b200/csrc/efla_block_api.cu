@@ -48,17 +48,18 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
 
 // ---------------------------------------------------------------- norm
 
-// Threads of a row and vectors of a thread for nvec vectors: the smallest
-// count of threads that takes the row in one vector each, up to 512 (with
-// 1024 a thread has 64 registers and the wide rows spill).
+// Threads of a row and vectors of a thread for nvec vectors: two vectors a
+// thread from 64 vectors on, so that the row's sums and root cost each
+// element less, and up to 512 threads (with 1024 a thread has 64 registers
+// and wide rows spill).
 #define EFLA_NORM_VEC(LAUNCH, T, nvec)                                     \
     do {                                                                   \
         if ((nvec) <= 16) { LAUNCH(16, 1); }                               \
         else if ((nvec) <= 32) { LAUNCH(32, 1); }                          \
-        else if ((nvec) <= 64) { LAUNCH(64, 1); }                          \
-        else if ((nvec) <= 128) { LAUNCH(128, 1); }                        \
-        else if ((nvec) <= 256) { LAUNCH(256, 1); }                        \
-        else if ((nvec) <= 512) { LAUNCH(512, 1); }                        \
+        else if ((nvec) <= 64) { LAUNCH(32, 2); }                          \
+        else if ((nvec) <= 128) { LAUNCH(64, 2); }                         \
+        else if ((nvec) <= 256) { LAUNCH(128, 2); }                        \
+        else if ((nvec) <= 512) { LAUNCH(256, 2); }                        \
         else if ((nvec) <= 1024) { LAUNCH(512, 2); }                       \
         else if ((nvec) <= 2048) { LAUNCH(512, 4); }                       \
         else if constexpr (sizeof(T) == 4) { LAUNCH(512, 8); }             \
@@ -90,7 +91,7 @@ template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdA
     // four rows in flight a thread once there are rows enough for two blocks an SM
 #define EFLA_L(TPR, IT)                                                                                     \
     do {                                                                                                    \
-        constexpr int SL = norm::kThreadsOf<TPR> / TPR, RPI = TPR <= 256 ? 4 : IT == 1 ? 2 : 1;             \
+        constexpr int SL = norm::kThreadsOf<TPR> / TPR, RPI = IT == 1 ? 4 : IT == 2 ? 2 : 1;                \
         if (a.rows >= 2LL * num_sms() * SL * RPI)                                                           \
             norm::norm_fwd_kernel<T, R, TPR, IT, RPI>                                                       \
                 <<<(unsigned)((a.rows + SL * RPI - 1) / (SL * RPI)), norm::kThreadsOf<TPR>, 0, st>>>(a);     \
@@ -117,7 +118,7 @@ template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdA
     }
     const int nvec = a.C / VEC;
 #define EFLA_L(TPR, IT) \
-    norm::norm_bwd_kernel<T, R, TPR, IT, (TPR <= 256 ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
+    norm::norm_bwd_kernel<T, R, TPR, IT, (IT == 1 ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
     EFLA_NORM_VEC(EFLA_L, T, nvec);
 #undef EFLA_L
     return launched();
@@ -264,31 +265,39 @@ template <typename T, typename S> bool scan_vec(const scan::Args &a) {
     return v;
 }
 
-template <typename T, typename S> efla_status_t launch_scan_fwd(scan::Args a, long long blocks, cudaStream_t st) {
-    a.vec = scan_vec<T, S>(a);
+template <typename T, typename S, bool VEC> efla_status_t run_scan_fwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
     if (a.nseg > 1) {
-        scan::segment_kernel<T, S, false><<<(unsigned)(blocks * a.nseg), scan::kThreads, 0, st>>>(a);
+        scan::segment_kernel<T, S, VEC, false><<<grid, scan::kThreads, 0, st>>>(a);
         if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
     }
-    scan::scan_fwd_kernel<T, S><<<(unsigned)(blocks * a.nseg), scan::kThreads, 0, st>>>(a);
+    scan::scan_fwd_kernel<T, S, VEC><<<grid, scan::kThreads, 0, st>>>(a);
+    return launched();
+}
+
+template <typename T, typename S> efla_status_t launch_scan_fwd(const scan::Args &a, long long blocks, cudaStream_t st) {
+    const unsigned grid = (unsigned)(blocks * a.nseg);
+    return scan_vec<T, S>(a) ? run_scan_fwd<T, S, true>(a, grid, st) : run_scan_fwd<T, S, false>(a, grid, st);
+}
+
+template <typename T, typename S, bool VEC> efla_status_t run_scan_bwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
+    constexpr size_t smem = sizeof(scan::BwdSmem<T, S>);
+    if (!ensure_smem<scan::scan_bwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
+    if (a.nseg > 1) {
+        scan::segment_kernel<T, S, VEC, false><<<grid, scan::kThreads, 0, st>>>(a);
+        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
+        scan::segment_kernel<T, S, VEC, true><<<grid, scan::kThreads, 0, st>>>(a);
+        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
+    }
+    scan::scan_bwd_kernel<T, S, VEC><<<grid, scan::kThreads, smem, st>>>(a);
     return launched();
 }
 
 template <typename T, typename S>
-efla_status_t launch_scan_bwd(scan::Args a, long long blocks, void *dB, void *dC, float *dA, float *dD, float *db,
-                              cudaStream_t st) {
-    a.vec = scan_vec<T, S>(a);
-    constexpr size_t smem = sizeof(scan::BwdSmem<T, S>);
-    if (!ensure_smem<scan::scan_bwd_kernel<T, S>>(smem)) return EFLA_ERR_CUDA;
+efla_status_t launch_scan_bwd(const scan::Args &a, long long blocks, void *dB, void *dC, float *dA, float *dD,
+                              float *db, cudaStream_t st) {
     const unsigned grid = (unsigned)(blocks * a.nseg);
-    if (a.nseg > 1) {
-        scan::segment_kernel<T, S, false><<<grid, scan::kThreads, 0, st>>>(a);
-        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
-        scan::segment_kernel<T, S, true><<<grid, scan::kThreads, 0, st>>>(a);
-        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
-    }
-    scan::scan_bwd_kernel<T, S><<<grid, scan::kThreads, smem, st>>>(a);
-    if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
+    efla_status_t s = scan_vec<T, S>(a) ? run_scan_bwd<T, S, true>(a, grid, st) : run_scan_bwd<T, S, false>(a, grid, st);
+    if (s != EFLA_OK) return s;
     const long long rows = (long long)a.B * a.L * a.G, quads = rows * 2 * a.N / 4;
     scan::scan_bc_kernel<T><<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(a.part_bc, static_cast<T *>(dB),
                                                                           static_cast<T *>(dC), rows, a.N, a.tpg);
@@ -336,7 +345,7 @@ efla_status_t efla_norm_fwd(const void *x, efla_dtype_t dtype, const void *res, 
         (overlaps(res_out, rb, y, xb) || overlaps(res_out, rb, y8, n) || overlaps(res_out, rb, scale, sb) ||
          (res_out == res ? overlaps(res, rb, x, xb) : overlaps(x, xb, res, rb))))
         return EFLA_ERR_ALIAS;
-    const norm::FwdArgs a{x, res, weight, y, res_out, static_cast<unsigned char *>(y8), scale, eps, group, C, rows};
+    const norm::FwdArgs a{x, res, weight, y, res_out, static_cast<unsigned char *>(y8), scale, eps, 1.f / C, group, C, rows};
     const bool vec = C % (16 / (int)esize(dtype)) == 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == EFLA_F32) return launch_norm_fwd<float, float>(a, vec, st);
@@ -371,7 +380,7 @@ efla_status_t efla_norm_bwd(const void *dy, efla_dtype_t dtype, const void *h, e
     const Buf out[] = {{dx, n * esize(dtype)}, {dres, n * esize(h_dtype)}, {dweight, (size_t)C * 4}, {workspace, need}};
     if (aliased(in, out)) return EFLA_ERR_ALIAS;
     float *part = static_cast<float *>(workspace);
-    const norm::BwdArgs a{dy, h, dres_out, weight, dx, dres, part, eps, C, rows};
+    const norm::BwdArgs a{dy, h, dres_out, weight, dx, dres, part, eps, 1.f / C, C, rows};
     const int blocks = (int)norm_bwd_blocks(rows);
     const bool vec = C % (16 / (int)esize(dtype)) == 0;
     efla_status_t s;
@@ -404,7 +413,7 @@ efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, co
     a.head = heads ? C / heads : 0;
     a.B = B; a.L = L; a.C = C; a.tiles = conv_tiles(L, conv::kRunFwd);
     a.y = y; a.state_out = state_out;
-    const int row = a.head ? a.head : C, VEC = 16 / (int)e;
+    const int row = a.head ? a.head : C, VEC = 4;
     const bool vec = row % VEC == 0 && rows_in_vectors(x, ldx, VEC, e);
     const dim3 grid((unsigned)(B * a.tiles), (unsigned)((C + 32 * (vec ? VEC : 1) - 1) / (32 * (vec ? VEC : 1))));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -412,7 +421,7 @@ efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, co
         if (vec) EFLA_CONV_K(conv::conv_fwd_kernel, float, 4, K, grid, 32 * conv::kWarps, a);
         else EFLA_CONV_K(conv::conv_fwd_kernel, float, 1, K, grid, 32 * conv::kWarps, a);
     } else {
-        if (vec) EFLA_CONV_K(conv::conv_fwd_kernel, __nv_bfloat16, 8, K, grid, 32 * conv::kWarps, a);
+        if (vec) EFLA_CONV_K(conv::conv_fwd_kernel, __nv_bfloat16, 4, K, grid, 32 * conv::kWarps, a);
         else EFLA_CONV_K(conv::conv_fwd_kernel, __nv_bfloat16, 1, K, grid, 32 * conv::kWarps, a);
     }
     return launched();

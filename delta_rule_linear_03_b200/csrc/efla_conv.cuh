@@ -20,7 +20,7 @@ namespace efla {
 namespace conv {
 
 constexpr int kWarps = 8;
-constexpr int kRunFwd = 16, kRunBwd = 32;  // tokens of one thread's run
+constexpr int kRunFwd = 32, kRunBwd = 32;  // tokens of one thread's run
 
 struct Args {
     const void *x;
@@ -50,6 +50,26 @@ __device__ __forceinline__ long long out_at(const Args &a, int b, long long t, i
     return (((long long)b * (a.C / a.head) + c / a.head) * a.L + t) * a.head + c % a.head;
 }
 
+// Filters w[j][i] of VEC channels from channel c on.
+template <int K, int VEC> __device__ __forceinline__ void load_filters(const float *p, int c, float (&w)[K][VEC]) {
+    float v[VEC * K];
+    p += (long long)c * K;
+    if constexpr (VEC * K % 4 == 0) {  // c is a multiple of VEC, so the filters begin on 16 bytes
+#pragma unroll
+        for (int i = 0; i < VEC * K; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC * K; ++i) v[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][i] = v[i * K + j];
+}
+
 template <typename T, int K, int VEC>
 __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(Args a) {
     constexpr int U = 4;  // rows in flight
@@ -65,11 +85,8 @@ __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(Args a) {
 
     float w[K][VEC], bias[VEC], win[K - 1][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = a.w[(long long)(c + i) * K + j];
-    }
+    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    load_filters<K, VEC>(a.w, c, w);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int t = t0 - (K - 1) + j;
@@ -156,11 +173,9 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
         for (int i = 0; i < VEC; ++i) {
             bias[i] = a.bias ? a.bias[c + i] : 0.f;
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
-                w[j][i] = a.w[(long long)(c + i) * K + j];
-                dwin[j][i] = 0.f;
-            }
+            for (int j = 0; j < K; ++j) dwin[j][i] = 0.f;
         }
+        load_filters<K, VEC>(a.w, c, w);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {  // x_{t0-K+1} .. x_{t0-1}, moved down by one when t0 itself comes in
             const int t = t0 - (K - 1) + j;

@@ -28,8 +28,14 @@ constexpr int kMaxC = 16384;
 
 template <int TPR> constexpr int kThreadsOf = TPR > 256 ? TPR : 256;
 
-// Sums (or maxima of non-negative floats' bit patterns, which order as the
-// floats do and keep a NaN) of V values over the TPR threads of a row.
+// The larger magnitude; a NaN stays one.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
+
+// Sums or maxima of V values over the TPR threads of a row.
 template <int TPR, int V> struct RowReduce {
     static constexpr int NW = kThreadsOf<TPR> / 32;
     float red[TPR > 32 ? V : 1][TPR > 32 ? NW : 1];
@@ -55,34 +61,58 @@ template <int TPR, int V> struct RowReduce {
             }
         }
     }
-    __device__ __forceinline__ void max_bits(uint32_t (&v)[V]) {
+    // largest of values that are magnitudes; a NaN stays one
+    __device__ __forceinline__ void max_abs(float (&v)[V]) {
 #pragma unroll
         for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = max(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+            for (int i = 0; i < V; ++i) v[i] = norm::max_abs(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
         if constexpr (TPR > 32) {
             const int warp = threadIdx.x >> 5;
             if ((threadIdx.x & 31) == 0)
 #pragma unroll
-                for (int i = 0; i < V; ++i) red[i][warp] = __uint_as_float(v[i]);
+                for (int i = 0; i < V; ++i) red[i][warp] = v[i];
             __syncthreads();
             const int w0 = warp / (TPR / 32) * (TPR / 32);
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int k = 0; k < TPR / 32; ++k) v[i] = max(v[i], __float_as_uint(red[i][w0 + k]));
+                for (int k = 0; k < TPR / 32; ++k) v[i] = norm::max_abs(v[i], red[i][w0 + k]);
         }
     }
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// 1 / sqrt(m): the approximate root's 2 ulp with one Newton step; 0 for an infinite m.
+__device__ __forceinline__ float rstd_of(float m) {
+    const float r = rsqrtf(m);
+    return m < __int_as_float(0x7f800000) ? r * fmaf(-0.5f * m * r, r, 1.5f) : m != m ? m : 0.f;
+}
 // A group's scale from its largest |y|; a NaN stays one.
-__device__ __forceinline__ float scale_of(uint32_t bits) {
-    const float a = __uint_as_float(bits) / kE4m3Max;
+__device__ __forceinline__ float scale_of(float top) {
+    const float a = top * (1.f / kE4m3Max);
     return a < kScaleMin ? kScaleMin : a;
 }
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+template <int N> __device__ __forceinline__ void widen2(const float (&v)[N], f32x2 (&o)[N / 2]) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) o[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+template <typename T, int N> __device__ __forceinline__ void widen2(const Raw<T, N> &r, f32x2 (&o)[N / 2]) {
+    float v[N];
+    widen<T, N>(r, v);
+    widen2<N>(v, o);
+}
+template <typename T, int N> __device__ __forceinline__ Raw<T, N> narrow2(const f32x2 (&p)[N / 2]) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 t = unpack2(p[i]);
+        v[2 * i] = t.x;
+        v[2 * i + 1] = t.y;
+    }
+    return narrow<T, N>(v);
 }
 
 struct FwdArgs {
@@ -91,7 +121,7 @@ struct FwdArgs {
     void *y, *res_out;
     unsigned char *y8;
     float *scale;
-    float eps;
+    float eps, inv_c;  // inv_c = 1 / C
     int group;  // columns of one scale: 128, or 0 for the row
     int C;
     long long rows;
@@ -120,48 +150,64 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
             xr[i][k] = in ? load_raw<T, VEC>(x + row * C + c) : zero_raw<T, VEC>();
             if (res) rr[i][k] = in ? load_raw<R, VEC>(res + row * C + c) : zero_raw<R, VEC>();
         }
-    float h[RPI][IT][VEC], ss[RPI];
+    f32x2 h[RPI][IT][VEC / 2];
+    float ss[RPI];
 #pragma unroll
     for (int i = 0; i < RPI; ++i) {
-        ss[i] = 0.f;
+        f32x2 s2 = 0ull;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            widen<T, VEC>(xr[i][k], h[i][k]);
-            if (res)
+            widen2<T, VEC>(xr[i][k], h[i][k]);
+            if (res) {
+                f32x2 r[VEC / 2];
+                widen2<R, VEC>(rr[i][k], r);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) h[i][k][j] += to_f32(rr[i][k].e[j]);
+                for (int j = 0; j < VEC / 2; ++j) h[i][k][j] = add2(h[i][k][j], r[j]);
+            }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) ss[i] = fmaf(h[i][k][j], h[i][k][j], ss[i]);
+            for (int j = 0; j < VEC / 2; ++j) s2 = fma2(h[i][k][j], h[i][k][j], s2);
         }
+        ss[i] = sum2(s2);
     }
-    float w[IT][VEC];
+    f32x2 w[IT][VEC / 2];
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
         const int c = (k * TPR + l) * VEC;
-        widen<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
+        widen2<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
     }
     rs.sum(ss);
-    uint32_t top[RPI];
+    // columns past C hold zeros, which are no part of a maximum (their product with an infinite
+    // or absent root is kept out)
+    float top[RPI];
 #pragma unroll
     for (int i = 0; i < RPI; ++i) {
         const long long row = row0 + i * SLOTS;
-        const float rstd = 1.f / sqrtf(ss[i] / (float)C + a.eps);
-        top[i] = 0u;
+        const float rstd = rstd_of(fmaf(ss[i], a.inv_c, a.eps));
+        top[i] = 0.f;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int c = (k * TPR + l) * VEC;
             const bool in = row < a.rows && c < C;
-            if (a.res_out && in) store_raw<R, VEC>(static_cast<R *>(a.res_out) + row * C + c, narrow<R, VEC>(h[i][k]));
+            if (a.res_out && in) store_raw<R, VEC>(static_cast<R *>(a.res_out) + row * C + c, narrow2<R, VEC>(h[i][k]));
+            const f32x2 r2 = in ? pack2(rstd, rstd) : 0ull;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                h[i][k][j] = in ? h[i][k][j] * rstd * w[k][j] : 0.f;  // columns past C: no part of a maximum
-                top[i] = max(top[i], abs_bits(h[i][k][j]));
-            }
-            if (a.y && in) store_raw<T, VEC>(static_cast<T *>(a.y) + row * C + c, narrow<T, VEC>(h[i][k]));
+            for (int j = 0; j < VEC / 2; ++j) h[i][k][j] = mul2(mul2(h[i][k][j], r2), w[k][j]);
+            if (a.y && in) store_raw<T, VEC>(static_cast<T *>(a.y) + row * C + c, narrow2<T, VEC>(h[i][k]));
         }
     }
     if (!a.y8) return;
-    if (!a.group) rm.max_bits(top);
+    if (!a.group) {
+#pragma unroll
+        for (int i = 0; i < RPI; ++i)
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const float2 t = unpack2(h[i][k][j]);
+                    top[i] = max_abs(max_abs(top[i], t.x), t.y);
+                }
+        rm.max_abs(top);
+    }
     const int ng = a.group ? (C + kGroup - 1) / kGroup : 1;
 #pragma unroll
     for (int i = 0; i < RPI; ++i) {
@@ -169,20 +215,25 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int c = (k * TPR + l) * VEC;
-            uint32_t m = top[i];
+            float m = top[i];
             if (a.group) {
-                m = 0u;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) m = max(m, abs_bits(h[i][k][j]));
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const float2 t = unpack2(h[i][k][j]);
+                    m = max_abs(max_abs(m, t.x), t.y);
+                }
 #pragma unroll
-                for (int o = LPG / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = LPG / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
             }
-            const float s = scale_of(m), inv = 1.f / s;
+            const float s = scale_of(m), inv = rcp(s);
             if (row >= a.rows || c >= C) continue;
             if (a.group ? l % LPG == 0 : (l == 0 && k == 0)) a.scale[row * ng + (a.group ? c / kGroup : 0)] = s;
             uint16_t q[VEC / 2];
 #pragma unroll
-            for (int j = 0; j < VEC; j += 2) q[j / 2] = e4m3x2(h[i][k][j] * inv, h[i][k][j + 1] * inv);
+            for (int j = 0; j < VEC / 2; ++j) {
+                const float2 t = unpack2(mul2(h[i][k][j], pack2(inv, inv)));
+                q[j] = e4m3x2(t.x, t.y);
+            }
             unsigned char *p = a.y8 + row * C + c;
             if constexpr (VEC == 8)
                 *reinterpret_cast<uint2 *>(p) =
@@ -219,8 +270,8 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_fwd_any_kernel(FwdA
 #pragma unroll
         for (int j = 0; j < 4; ++j) ss[0] = fmaf(h[k][j], h[k][j], ss[0]);
     rs.sum(ss);
-    const float rstd = 1.f / sqrtf(ss[0] / (float)C + a.eps);
-    uint32_t top[1] = {0u};
+    const float rstd = rstd_of(fmaf(ss[0], a.inv_c, a.eps));
+    float top[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < IT; ++k)
 #pragma unroll
@@ -233,22 +284,22 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_fwd_any_kernel(FwdA
             if (a.res_out) static_cast<R *>(a.res_out)[row * C + c] = from_f32<R>(h[k][j]);
             h[k][j] = h[k][j] * rstd * a.w[c];
             if (a.y) static_cast<T *>(a.y)[row * C + c] = from_f32<T>(h[k][j]);
-            top[0] = max(top[0], abs_bits(h[k][j]));
+            top[0] = max_abs(top[0], h[k][j]);
         }
     if (!a.y8) return;
-    if (!a.group) rm.max_bits(top);
+    if (!a.group) rm.max_abs(top);
     const int ng = a.group ? (C + kGroup - 1) / kGroup : 1;
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-        uint32_t m = top[0];
+        float m = top[0];
         if (a.group) {
-            m = 0u;
+            m = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) m = max(m, abs_bits(h[k][j]));
+            for (int j = 0; j < 4; ++j) m = max_abs(m, h[k][j]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
         }
-        const float s = scale_of(m), inv = 1.f / s;
+        const float s = scale_of(m), inv = rcp(s);
         const int g = k * WPR + wr;
         if (!on || g * kGroup >= C) continue;
         if (lane == 0 && (a.group || g == 0)) a.scale[row * ng + (a.group ? g : 0)] = s;
@@ -265,7 +316,7 @@ struct BwdArgs {
     const float *w;
     void *dx, *dres;  // dx in the type of dy, dres in the type of h; either may be NULL
     float *part;      // [blocks][C]
-    float eps;
+    float eps, inv_c;
     int C;
     long long rows;
 };
@@ -321,8 +372,8 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < RPI; ++i) {
             const long long row = base + i * SLOTS + slot;
-            const float rstd = 1.f / sqrtf(s[2 * i] / (float)C + a.eps);
-            const float m = rstd * rstd * (s[2 * i + 1] / (float)C);
+            const float rstd = rstd_of(fmaf(s[2 * i], a.inv_c, a.eps));
+            const float m = rstd * rstd * (s[2 * i + 1] * a.inv_c);
 #pragma unroll
             for (int k = 0; k < IT; ++k) {
                 const int c = (k * TPR + l) * VEC;
@@ -401,8 +452,8 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdA
                 s[1] = fmaf(yv[k][j] * w[k][j], hv[k][j], s[1]);
             }
         rs[par].sum(s);
-        const float rstd = 1.f / sqrtf(s[0] / (float)C + a.eps);
-        const float m = rstd * rstd * (s[1] / (float)C);
+        const float rstd = rstd_of(fmaf(s[0], a.inv_c, a.eps));
+        const float m = rstd * rstd * (s[1] * a.inv_c);
 #pragma unroll
         for (int k = 0; k < IT; ++k)
 #pragma unroll

@@ -37,7 +37,6 @@ namespace efla {
 namespace scan {
 
 constexpr int kThreads = 128;
-constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Args {
     const void *x, *dt, *z, *Bm, *Cm;
@@ -46,7 +45,7 @@ struct Args {
     const int *lengths;
     void *y;
     float *h_L;
-    int softplus, vec;  // vec: every row can be read and written in whole vectors
+    int softplus, vec;  // vec: scan_step_kernel reads B and C in vectors of four
     int B, L, C, G, N;
     int tpg;            // channel tiles of a group
     int nseg, seg;      // segments, and tokens of one (a multiple of the tile)
@@ -66,6 +65,7 @@ struct Args {
 
 template <int N_, int NS_> struct Shape {
     static constexpr int N = N_, NS = NS_;
+    static constexpr int NP = NS / 2;                  // register pairs of a lane's state
     static constexpr int LN = N / NS;                  // lanes of a channel
     static constexpr int LC = 32 / LN;                 // channels of a warp
     static constexpr int CT = kThreads / LN;           // channels of a block
@@ -75,29 +75,38 @@ template <int N_, int NS_> struct Shape {
     static constexpr int BPT = TC * N / kThreads;      // values of B (and of C) that a thread loads
     static constexpr int TB = LN < 8 ? LN : 8;         // tokens whose sums are taken together
     static constexpr int PAD = CT % 32 == 0 ? 8 : CT / 4;  // sums of TB tokens go to different banks
+    static constexpr int CS = CT + PAD;
+
+    // Column of channel c of token t in the rows of 16-byte entries that pass
+    // D and D x on: a thread writes EPT neighbours one after the other, so
+    // neighbouring threads' entries are put into different banks.
+    __device__ static __forceinline__ int column(int c, int t) {
+        return c ^ (c >> 3 & 7) ^ ((t & 1) * (EPT / 2));
+    }
 };
 
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// softplus(v) = max(v, 0) + log1p(e^-|v|), log1p(e) = 2 atanh(e / (2 + e)) by
-// its series: the argument is at most 1/3, so eight terms leave less than
-// 2^-29 of the result.
+// softplus(v) = max(v, 0) + log1p(e), e = e^-|v|, by log1p(e) = 2 atanh(s),
+// s = e / (2 + e) <= 1/3, whose series s + s^3/3 + ... + s^13/13 leaves less
+// than 2^-26 of it.  A step's error goes into every decay of its token, so e
+// and s are taken to the last bits: what the argument's product with log2 e
+// loses is put back to first order, and the quotient has one Newton step.
 __device__ __forceinline__ float softplus_f32(float v) {
-    const float e = __expf(-fabsf(v));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
+    const float a = fabsf(v) > 126.f ? -126.f : -fabsf(v), t = a * kLog2e;  // e is 0 from there on; NaN stays
+    const float lo = fmaf(a, 1.925963e-8f, fmaf(a, kLog2e, -t));              // the rounding of log2 e, that of the product
+    float e = ex2(t);
+    e = fmaf(e * lo, 0.6931472f, e);
+    const float w = 2.f + e, r = rcp(w);
+    float s = e * r;
+    s = fmaf(fmaf(-s, w, e), r, s);
+    const float q = s * s;
+    float p = 1.f / 13.f;
     p = fmaf(p, q, 1.f / 11.f);
     p = fmaf(p, q, 1.f / 9.f);
     p = fmaf(p, q, 1.f / 7.f);
     p = fmaf(p, q, 1.f / 5.f);
     p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaxf(v, 0.f) + 2.f * s * p;
+    const float s2 = s + s;
+    return fmaxf(v, 0.f) + fmaf(p * q, s2, s2);
 }
 
 // Sums v[0..V) over the 2^k lanes that differ in the bits of [STEP, LIM).
@@ -156,258 +165,362 @@ struct Where {
     }
 };
 
-// EPT neighbouring channels of one token; zeros where the token or channel is none.
-template <typename T, int EPT>
-__device__ __forceinline__ Raw<T, EPT> load_row(const void *base, long long ld, long long row, int c, int n, bool on,
-                                                bool vec) {
-    if (!on || n <= 0) return zero_raw<T, EPT>();
-    const T *p = static_cast<const T *>(base) + row * ld + c;
-    return vec ? load_raw<T, EPT>(p) : load_raw_any<T, EPT>(p, n);
+// EPT neighbouring channels, from channel pc on, of a row of nc; what lies past
+// the row's end repeats a channel of it.  VEC: pc and nc are multiples of EPT
+// and the row is aligned for whole vectors.  Rows are read whether or not
+// their token counts: a load without a condition can be issued a tile ahead.
+template <typename T, int EPT, bool VEC>
+__device__ __forceinline__ Raw<T, EPT> load_row(const T *row, int pc, int nc) {
+    if constexpr (VEC) {
+        return load_raw<T, EPT>(row + (pc < nc ? pc : 0));
+    } else {
+        Raw<T, EPT> r;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) r.e[i] = row[min(pc + i, nc - 1)];
+        return r;
+    }
+}
+template <typename T, int BPT, bool VEC> __device__ __forceinline__ Raw<T, BPT> load_bc(const T *p) {
+    if constexpr (VEC) {
+        return load_raw<T, BPT>(p);
+    } else {
+        Raw<T, BPT> r;
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) r.e[i] = p[i];
+        return r;
+    }
 }
 
-// BPT values of a token's B or C of one group, as they lie in memory.
-template <typename T, typename S>
-__device__ __forceinline__ Raw<T, S::BPT> load_bc(const void *base, long long ld, long long row, int off, bool on,
-                                                  bool vec) {
-    if (!on) return zero_raw<T, S::BPT>();
-    const T *p = static_cast<const T *>(base) + row * ld + off;
-    return vec ? load_raw<T, S::BPT>(p) : load_raw_any<T, S::BPT>(p, S::BPT);
+// A lane's state values as register pairs, from and to shared or global memory.
+template <int NP> __device__ __forceinline__ void load_pairs(const float *p, f32x2 (&v)[NP]) {
+    if constexpr (NP == 2) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p);
+        v[0] = u.x;
+        v[1] = u.y;
+    } else {
+        v[0] = *reinterpret_cast<const f32x2 *>(p);
+    }
+}
+template <int NP> __device__ __forceinline__ void store_pairs(float *p, const f32x2 (&v)[NP]) {
+    if constexpr (NP == 2) *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v[0], v[1]);
+    else *reinterpret_cast<f32x2 *>(p) = v[0];
 }
 
-// The composed state before segment `seg`, for one lane's values.
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return pack2(ex2(t.x), ex2(t.y));
+}
+
+// Register j of a lane holds state n0 + (j ^ x); x is 0 but in the backward pass.
+template <typename S> __device__ __forceinline__ void gather(const float *p, int x, f32x2 (&v)[S::NP]) {
+#pragma unroll
+    for (int j = 0; j < S::NP; ++j) v[j] = pack2(p[(2 * j) ^ x], p[(2 * j + 1) ^ x]);
+}
+template <typename S> __device__ __forceinline__ void scatter(float *p, int x, const f32x2 (&v)[S::NP]) {
+#pragma unroll
+    for (int j = 0; j < S::NP; ++j) {
+        const float2 t = unpack2(v[j]);
+        p[(2 * j) ^ x] = t.x;
+        p[(2 * j + 1) ^ x] = t.y;
+    }
+}
+
+// The state before the block's segment, composed of the segments before it.
 template <typename S>
-__device__ __forceinline__ void start_state(const Args &a, const Where &w, int c, int n0, const float (&A2)[S::NS],
-                                            float (&h)[S::NS]) {
+__device__ __forceinline__ void start_state(const Args &a, const Where &w, int c, int n0, int x,
+                                            const f32x2 (&A2)[S::NP], f32x2 (&h)[S::NP]) {
     const long long bc = (long long)w.b * a.C + c, stride = (long long)a.B * a.C;
-#pragma unroll
-    for (int j = 0; j < S::NS; ++j) h[j] = 0.f;
-    const float *h0 = a.nseg > 1 ? a.seg_0 : a.h0;
     if (w.seg == 0) {
-        if (a.h0)
-#pragma unroll
-            for (int j = 0; j < S::NS; ++j) h[j] = h0[bc * S::N + n0 + j];
+        if (a.h0) gather<S>((a.nseg > 1 ? a.seg_0 : a.h0) + bc * S::N + n0, x, h);
         return;
     }
     for (int s = 0; s < w.seg; ++s) {
         const float d = a.seg_d[s * stride + bc];
+        f32x2 own[S::NP];
+        gather<S>(a.seg_h + (s * stride + bc) * S::N + n0, x, own);
 #pragma unroll
-        for (int j = 0; j < S::NS; ++j) h[j] = fmaf(ex2(d * A2[j]), h[j], a.seg_h[(s * stride + bc) * S::N + n0 + j]);
+        for (int j = 0; j < S::NP; ++j) h[j] = fma2(ex2_2(mul2(pack2(d, d), A2[j])), h[j], own[j]);
     }
+}
+
+// A thread's part in a tile: the token and channels it prepares, the token
+// and indices of B and C it loads.
+template <typename T, typename S> struct Part {
+    int pt, pc, bt, bn;
+    __device__ __forceinline__ Part(int tid)
+        : pt(tid / S::VPR), pc(tid % S::VPR * S::EPT), bt(tid * S::BPT / S::N), bn(tid * S::BPT % S::N) {}
+};
+
+// D and D x of a token's channels, each twice, as the lanes' paired operations take them.
+template <typename S>
+__device__ __forceinline__ void put_steps(float4 (*sd)[S::CT], int pt, int pc, const float (&d)[S::EPT],
+                                          const float (&u)[S::EPT]) {
+#pragma unroll
+    for (int e = 0; e < S::EPT; ++e) sd[pt][S::column(pc + e, pt)] = make_float4(d[e], d[e], u[e], u[e]);
 }
 
 // ---------------------------------------------------------------- one segment's own maps
 // REV = false: the final state from zero (the first segment: from h0) and the
 // sum of D.  REV = true: the adjoint that leaves the segment at its start
 // when none enters at its end (u_t = C_t g_t, p <- exp(D_t A) (p + u_t)).
-template <typename T, typename S, bool REV>
+template <typename T, typename S, bool VEC, bool REV>
 __global__ void __launch_bounds__(kThreads) segment_kernel(Args a) {
-    __shared__ float2 sd[S::TC][S::CT + S::PAD];  // D, D x (or g)
+    __shared__ float4 sd[S::TC][S::CT];  // D, D, and D x (or g) twice
     __shared__ __align__(16) float sb[S::TC][S::N];
+    constexpr int NP = S::NP;
     const Where w(a, S::CT);
+    const Part<T, S> part(threadIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
-    const int c = w.c0 + cl, n0 = ln * S::NS;
+    const int c = w.c0 + cl, n0 = ln * S::NS, pt = part.pt, pc = part.pc;
     const bool on = cl < w.nc;
-    float A2[S::NS], h[S::NS], sum = 0.f;
+    f32x2 A2[NP], h[NP];
+    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < S::NS; ++j) {
-        A2[j] = on ? a.A[(long long)c * S::N + n0 + j] * kLog2e : 0.f;
-        h[j] = 0.f;
-    }
+    for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
     const long long bc = (long long)w.b * a.C + c;
-    if (!REV && w.seg == 0 && a.h0 && on)
-#pragma unroll
-        for (int j = 0; j < S::NS; ++j) {
-            h[j] = a.h0[bc * S::N + n0 + j];
-            a.seg_0[bc * S::N + n0 + j] = h[j];
+    if (on) {
+        gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
+        if (!REV && w.seg == 0 && a.h0) {
+            gather<S>(a.h0 + bc * S::N + n0, 0, h);
+            scatter<S>(a.seg_0 + bc * S::N + n0, 0, h);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], pack2(kLog2e, kLog2e));
     const int end = min(w.t1, w.len);
-    const int pt = tid / S::VPR, pc = (tid % S::VPR) * S::EPT;  // this thread's token and channels of a tile
-    const int bt = tid * S::BPT / S::N, bn = tid * S::BPT % S::N;
     const int tiles = end > w.t0 ? (end - w.t0 + S::TC - 1) / S::TC : 0;
     float bias[S::EPT];
 #pragma unroll
     for (int i = 0; i < S::EPT; ++i) bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
 
+    const long long ldx = REV ? a.C : a.ldx, ldb = REV ? a.ldc : a.ldb, ldz = a.z ? a.ldz : ldx;
+    const T *px = static_cast<const T *>(REV ? a.dy : a.x) + w.c0;
+    const T *pd = static_cast<const T *>(a.dt) + w.c0;
+    const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+    const T *pb = static_cast<const T *>(REV ? a.Cm : a.Bm) + w.g * S::N + part.bn;
     Raw<T, S::EPT> rx, rd, rz;
     Raw<T, S::BPT> rb;
     const auto load = [&](int k) {
         const int t = w.t0 + k * S::TC;
-        const long long row = (long long)w.b * a.L + t + pt, rowb = (long long)w.b * a.L + t + bt;
-        const bool in = t + pt < end;
-        rx = load_row<T, S::EPT>(REV ? a.dy : a.x, REV ? (long long)a.C : a.ldx, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rd = load_row<T, S::EPT>(a.dt, a.lddt, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        if (REV && a.z) rz = load_row<T, S::EPT>(a.z, a.ldz, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rb = load_bc<T, S>(REV ? a.Cm : a.Bm, REV ? a.ldc : a.ldb, rowb, w.g * S::N + bn, t + bt < end, a.vec);
+        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1);
+        rx = load_row<T, S::EPT, VEC>(px + row * ldx, pc, w.nc);
+        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+        if (REV) rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+        rb = load_bc<T, S::BPT, VEC>(pb + ((long long)w.b * a.L + min(t + part.bt, a.L - 1)) * ldb);
     };
     if (tiles) load(REV ? tiles - 1 : 0);
+    const float4 *d0 = &sd[0][S::column(cl, 0)], *d1 = &sd[0][S::column(cl, 1)];
     for (int i = 0; i < tiles; ++i) {
-        const int k = REV ? tiles - 1 - i : i;
-        const bool in = w.t0 + k * S::TC + pt < end;
+        const int k = REV ? tiles - 1 - i : i, t0 = w.t0 + k * S::TC;
+        {
+            const bool in = t0 + pt < end, inb = t0 + part.bt < end;
+            float x[S::EPT], d[S::EPT], b[S::BPT];
+            widen<T, S::EPT>(rx, x);
+            widen<T, S::EPT>(rd, d);
+            widen<T, S::BPT>(rb, b);
+            if constexpr (REV) {
+                float z[S::EPT];
+                widen<T, S::EPT>(rz, z);
+                if (a.z)
 #pragma unroll
-        for (int e = 0; e < S::EPT; ++e) {
-            const float v = to_f32(rd.e[e]) + bias[e];
-            const float d = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
-            const float u = to_f32(rx.e[e]);
-            sd[pt][pc + e] = make_float2(d, REV ? (a.z ? u * silu_f32(to_f32(rz.e[e])) : u) : d * u);
+                    for (int e = 0; e < S::EPT; ++e) x[e] *= silu_f32(z[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < S::EPT; ++e) {
+                d[e] += bias[e];
+                d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+                x[e] = in ? (REV ? x[e] : d[e] * x[e]) : 0.f;
+            }
+            put_steps<S>(sd, pt, pc, d, x);
+#pragma unroll
+            for (int e = 0; e < S::BPT; ++e) b[e] = inb ? b[e] : 0.f;
+            store_raw<float, S::BPT>(&sb[part.bt][part.bn], narrow<float, S::BPT>(b));
         }
-#pragma unroll
-        for (int e = 0; e < S::BPT; ++e) sb[bt][bn + e] = to_f32(rb.e[e]);
         __syncthreads();
         if (i + 1 < tiles) load(REV ? k - 1 : k + 1);
 #pragma unroll 8
         for (int s = 0; s < S::TC; ++s) {
             const int t = REV ? S::TC - 1 - s : s;
-            const float2 d = sd[t][cl];
-            sum += d.x;
+            const float4 d = (t & 1 ? d1 : d0)[t * S::CT];
+            f32x2 b[NP];
+            load_pairs<NP>(&sb[t][n0], b);
+            if (!REV) sum += d.x;
+            const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
 #pragma unroll
-            for (int j = 0; j < S::NS; ++j) {
-                const float e = ex2(d.x * A2[j]), u = d.y * sb[t][n0 + j];
-                h[j] = REV ? e * (h[j] + u) : fmaf(e, h[j], u);
+            for (int j = 0; j < NP; ++j) {
+                const f32x2 e = ex2_2(mul2(dd, A2[j]));
+                h[j] = REV ? mul2(e, fma2(uu, b[j], h[j])) : fma2(e, h[j], mul2(uu, b[j]));
             }
         }
         __syncthreads();
     }
     if (!on) return;
     const long long at = (long long)w.seg * a.B * a.C + bc;
-    float *out = (REV ? a.seg_p : a.seg_h) + at * S::N + n0;
-#pragma unroll
-    for (int j = 0; j < S::NS; ++j) out[j] = h[j];
+    scatter<S>((REV ? a.seg_p : a.seg_h) + at * S::N + n0, 0, h);
     if (!REV && ln == 0) a.seg_d[at] = sum;
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T, typename S> __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(Args a) {
-    __shared__ float2 sd[S::TC][S::CT + S::PAD];  // D, D x
-    __shared__ float sy[S::TC][S::CT + S::PAD];   // <C, h>
+template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(Args a) {
+    __shared__ float4 sd[S::TC][S::CT];               // D, D, D x, D x
+    __shared__ __align__(16) float sy[S::TC][S::CS];  // <C, h>
     __shared__ __align__(16) float sb[S::TC][S::N], sc[S::TC][S::N];
+    constexpr int NP = S::NP;
     const Where w(a, S::CT);
+    const Part<T, S> part(threadIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
-    const int c = w.c0 + cl, n0 = ln * S::NS;
+    const int c = w.c0 + cl, n0 = ln * S::NS, pt = part.pt, pc = part.pc;
     const bool on = cl < w.nc;
-    float A2[S::NS], h[S::NS];
+    f32x2 A2[NP], h[NP];
 #pragma unroll
-    for (int j = 0; j < S::NS; ++j) {
-        A2[j] = on ? a.A[(long long)c * S::N + n0 + j] * kLog2e : 0.f;
-        h[j] = 0.f;
-    }
-    if (on) start_state<S>(a, w, c, n0, A2, h);
+    for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
+    if (on) gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], pack2(kLog2e, kLog2e));
+    if (on) start_state<S>(a, w, c, n0, 0, A2, h);
     const int end = min(w.t1, w.len);
-    const int pt = tid / S::VPR, pc = (tid % S::VPR) * S::EPT;
-    const int bt = tid * S::BPT / S::N, bn = tid * S::BPT % S::N;
     float bias[S::EPT], dskip[S::EPT];
 #pragma unroll
     for (int i = 0; i < S::EPT; ++i) {
         bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
         dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
     }
+    const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
+    const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+    const long long ldz = a.z ? a.ldz : a.ldx;
+    const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
     Raw<T, S::EPT> rx, rd, rz;
     Raw<T, S::BPT> rb, rc;
     const auto load = [&](int t) {
-        const long long row = (long long)w.b * a.L + t + pt, rowb = (long long)w.b * a.L + t + bt;
-        const bool in = t + pt < end, inb = t + bt < end;
-        rx = load_row<T, S::EPT>(a.x, a.ldx, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rd = load_row<T, S::EPT>(a.dt, a.lddt, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        if (a.z) rz = load_row<T, S::EPT>(a.z, a.ldz, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rb = load_bc<T, S>(a.Bm, a.ldb, rowb, w.g * S::N + bn, inb, a.vec);
-        rc = load_bc<T, S>(a.Cm, a.ldc, rowb, w.g * S::N + bn, inb, a.vec);
+        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
+        rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
+        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+        rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+        rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
+        rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
     };
     load(w.t0);
+    const float4 *d0 = &sd[0][S::column(cl, 0)], *d1 = &sd[0][S::column(cl, 1)];
+    float *out = &sy[halved_index<S::TB, 1, S::LN>(lane)][cl];
     for (int t = w.t0; t < w.t1; t += S::TC) {
         const Raw<T, S::EPT> cx = rx, cz = rz;
         const bool in = t + pt < end;
+        {
+            const bool inb = t + part.bt < end;
+            float x[S::EPT], d[S::EPT], b[S::BPT], q[S::BPT];
+            widen<T, S::EPT>(rx, x);
+            widen<T, S::EPT>(rd, d);
+            widen<T, S::BPT>(rb, b);
+            widen<T, S::BPT>(rc, q);
 #pragma unroll
-        for (int e = 0; e < S::EPT; ++e) {
-            const float v = to_f32(rd.e[e]) + bias[e];
-            const float d = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
-            sd[pt][pc + e] = make_float2(d, d * to_f32(rx.e[e]));
-        }
+            for (int e = 0; e < S::EPT; ++e) {
+                d[e] += bias[e];
+                d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+                x[e] = in ? d[e] * x[e] : 0.f;
+            }
+            put_steps<S>(sd, pt, pc, d, x);
 #pragma unroll
-        for (int e = 0; e < S::BPT; ++e) {
-            sb[bt][bn + e] = to_f32(rb.e[e]);
-            sc[bt][bn + e] = to_f32(rc.e[e]);
+            for (int e = 0; e < S::BPT; ++e) {
+                b[e] = inb ? b[e] : 0.f;
+                q[e] = inb ? q[e] : 0.f;
+            }
+            store_raw<float, S::BPT>(&sb[part.bt][part.bn], narrow<float, S::BPT>(b));
+            store_raw<float, S::BPT>(&sc[part.bt][part.bn], narrow<float, S::BPT>(q));
         }
         __syncthreads();
         if (t + S::TC < w.t1) load(t + S::TC);
         if (t < end) {
-#pragma unroll 1
+#pragma unroll 2
             for (int s = 0; s < S::TC; s += S::TB) {
                 float p[S::TB];
 #pragma unroll
                 for (int u = 0; u < S::TB; ++u) {
-                    const float2 d = sd[s + u][cl];
-                    p[u] = 0.f;
+                    const float4 d = (u & 1 ? d1 : d0)[(s + u) * S::CT];
+                    const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
+                    f32x2 b[NP], q[NP], y = 0ull;
+                    load_pairs<NP>(&sb[s + u][n0], b);
+                    load_pairs<NP>(&sc[s + u][n0], q);
 #pragma unroll
-                    for (int j = 0; j < S::NS; ++j) {
-                        h[j] = fmaf(ex2(d.x * A2[j]), h[j], d.y * sb[s + u][n0 + j]);
-                        p[u] = fmaf(h[j], sc[s + u][n0 + j], p[u]);
+                    for (int j = 0; j < NP; ++j) {
+                        h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
+                        y = j ? fma2(h[j], q[j], y) : mul2(h[j], q[j]);
                     }
+                    p[u] = sum2(y);
                 }
                 halve<S::TB, 1, S::LN>(p, lane);
-                if (S::LN <= S::TB || ln < S::TB) sy[s + halved_index<S::TB, 1, S::LN>(lane)][cl] = p[0];
+                if (S::LN <= S::TB || ln < S::TB) out[s * S::CS] = p[0];
             }
         }
         __syncthreads();
         if (t + pt < w.t1 && pc < w.nc) {
-            float o[S::EPT];
+            float x[S::EPT], z[S::EPT], o[S::EPT];
+            widen<T, S::EPT>(cx, x);
+            widen<T, S::EPT>(cz, z);
+            widen<float, S::EPT>(load_raw<float, S::EPT>(&sy[pt][pc]), o);
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                o[e] = 0.f;
-                if (in) {
-                    o[e] = fmaf(dskip[e], to_f32(cx.e[e]), sy[pt][pc + e]);
-                    if (a.z) o[e] *= silu_f32(to_f32(cz.e[e]));
-                }
+                o[e] = fmaf(dskip[e], x[e], o[e]);
+                if (a.z) o[e] *= silu_f32(z[e]);
+                o[e] = in ? o[e] : 0.f;
             }
             T *y = static_cast<T *>(a.y) + ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
-            if (a.vec) store_raw<T, S::EPT>(y, narrow<T, S::EPT>(o));
+            if constexpr (VEC) store_raw<T, S::EPT>(y, narrow<T, S::EPT>(o));
             else store_raw_any<T, S::EPT>(y, narrow<T, S::EPT>(o), w.nc - pc);
         }
     }
-    if (a.h_L && on && w.seg == a.nseg - 1)
-#pragma unroll
-        for (int j = 0; j < S::NS; ++j) a.h_L[((long long)w.b * a.C + c) * S::N + n0 + j] = h[j];
+    if (a.h_L && on && w.seg == a.nseg - 1) scatter<S>(a.h_L + ((long long)w.b * a.C + c) * S::N + n0, 0, h);
 }
 
 // ---------------------------------------------------------------- backward
 // Two walks over the segment.  The first repeats the forward recurrence and
-// leaves the state before every kSub-th token in the workspace, one float
-// vector a thread, where the second finds it in reverse order.  The second
-// goes backwards: for kSub tokens at a time it recomputes decays and states
-// into registers from that state, and then runs the adjoint down through
-// them.  Sums over channels (dB, dC) are taken by halving over a warp's
-// channel lanes, then over the block's warps in shared memory, and reach the
-// workspace as one partial row a block; those and the sums over sequences
-// (dA, dD, ddt_bias) are added by kernels of their own in a fixed order.
+// leaves the state before every kSub-th token in the workspace, one vector a
+// thread, where the second finds it in reverse order.  The second goes
+// backwards: for kSub tokens at a time it recomputes decays and states into
+// registers from that state, and then runs the adjoint down through them.
+//
+// dB and dC are sums over channels: a lane's 2 NS products of a token are
+// halved over the warp's channel lanes, then added over the block's warps in
+// shared memory, and reach the workspace as one partial row a block; those
+// and the sums over sequences (dA, dD, ddt_bias) are added by kernels of
+// their own in a fixed order.  So that halving needs no selection, a lane
+// whose channel bit says "keep the upper half" has its state values in the
+// registers in swapped order (register j: state n0 + (j ^ x)), and reads B
+// and C from a copy in that order.
 constexpr int kSub = 8;
 
 template <typename T, typename S> struct BwdSmem {
-    float sdx[S::TC][S::CT + S::PAD], sdd[S::TC][S::CT + S::PAD], sg[S::TC][S::CT + S::PAD];  // D x, D, g
-    float s1[S::TC][S::CT + S::PAD], s2[S::TC][S::CT + S::PAD], s3[S::TC][S::CT + S::PAD];    // <p,B>, <p e h,A>, <C,h>
-    alignas(16) float sb[S::TC][S::N];
-    alignas(16) float sc[S::TC][S::N];
-    float bc[kThreads / 32][S::TC][2][S::N];  // a warp's sums over its channels
+    static constexpr int COPY = S::TC * S::N + 16;  // one order's copy; the next begins 16 banks on
+    float4 sd[S::TC][S::CT];                        // D, D, D x, D x
+    float2 sg[S::TC][S::CT];                        // g, g
+    alignas(16) float s1[S::TC][S::CS];             // <p, B>
+    alignas(16) float s2[S::TC][S::CS];             // <p e h, A>
+    alignas(16) float s3[S::TC][S::CS];             // <C, h>
+    alignas(16) float sb[S::NS][COPY];
+    alignas(16) float sc[S::NS][COPY];
+    float bc[kThreads / 32][S::TC][2][S::N];        // a warp's sums over its channels
 };
 
-template <typename T, typename S> __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Args a) {
+template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     BwdSmem<T, S> &sm = *reinterpret_cast<BwdSmem<T, S> *>(raw_smem);
-    constexpr int NS = S::NS, LN = S::LN, TC = S::TC;
+    constexpr int NS = S::NS, NP = S::NP, LN = S::LN, TC = S::TC, TB = S::TB;
     const Where w(a, S::CT);
+    const Part<T, S> part(threadIdx.x);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN, cl = warp * S::LC + lane / LN;
-    const int c = w.c0 + cl, n0 = ln * NS;
+    const int c = w.c0 + cl, n0 = ln * NS, pt = part.pt, pc = part.pc;
+    const int ox = halved_index<NS, LN, 32>(lane);  // the order of this lane's states
     const bool on = cl < w.nc;
     const long long bc = (long long)w.b * a.C + c;
-    float A2[NS], A1[NS], h[NS], p[NS], dA[NS];
+    const f32x2 l2e = pack2(kLog2e, kLog2e), minus = pack2(-1.f, -1.f);
+    f32x2 A1[NP], A2[NP], h[NP], p[NP], dA[NP], lost[NP];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        A1[j] = on ? a.A[(long long)c * S::N + n0 + j] : 0.f;
-        A2[j] = A1[j] * kLog2e;
-        h[j] = p[j] = dA[j] = 0.f;
-    }
-    if (on) start_state<S>(a, w, c, n0, A2, h);
+    for (int j = 0; j < NP; ++j) A1[j] = h[j] = p[j] = dA[j] = lost[j] = 0ull;
+    if (on) gather<S>(a.A + (long long)c * S::N + n0, ox, A1);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) A2[j] = mul2(A1[j], l2e);
+    if (on) start_state<S>(a, w, c, n0, ox, A2, h);
     const int end = min(w.t1, w.len);
     const int tiles = end > w.t0 ? (end - w.t0 + TC - 1) / TC : 0;
-    const int pt = tid / S::VPR, pc = (tid % S::VPR) * S::EPT;
-    const int bt = tid * S::BPT / S::N, bn = tid * S::BPT % S::N;
     float bias[S::EPT], dskip[S::EPT], aD[S::EPT], ab[S::EPT];
 #pragma unroll
     for (int i = 0; i < S::EPT; ++i) {
@@ -416,42 +529,77 @@ template <typename T, typename S> __global__ void __launch_bounds__(kThreads) sc
         aD[i] = ab[i] = 0.f;
     }
     float *ck = a.ckpt + ((long long)blockIdx.x * (a.seg / kSub) * kThreads + tid) * NS;
-    const auto put = [&](int k, const float(&v)[NS]) {
-        store_raw<float, NS>(ck + (long long)k * kThreads * NS, narrow<float, NS>(v));
-    };
 
+    const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
+    const T *py = static_cast<const T *>(a.dy) + w.c0, *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+    const long long ldz = a.z ? a.ldz : a.ldx;
+    const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
     Raw<T, S::EPT> rx, rd, rz, ry;
     Raw<T, S::BPT> rb, rc;
-    const auto load_fwd = [&](int t) {
-        const long long row = (long long)w.b * a.L + t + pt, rowb = (long long)w.b * a.L + t + bt;
-        const bool in = t + pt < end;
-        rx = load_row<T, S::EPT>(a.x, a.ldx, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rd = load_row<T, S::EPT>(a.dt, a.lddt, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rb = load_bc<T, S>(a.Bm, a.ldb, rowb, w.g * S::N + bn, t + bt < end, a.vec);
+    const auto load = [&](int t, bool back) {
+        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
+        rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
+        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+        rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
+        if (back) {
+            ry = load_row<T, S::EPT, VEC>(py + row * a.C, pc, w.nc);
+            rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+            rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+        }
     };
-    if (tiles) load_fwd(w.t0);
-    for (int i = 0; i < tiles; ++i) {
-        const int t = w.t0 + i * TC;
-        const bool in = t + pt < end;
+    // B or C of the tile, zeros past the end, in every lane's order
+    const auto put_bc = [&](float (*to)[BwdSmem<T, S>::COPY], const Raw<T, S::BPT> &r, bool inb) {
+        float v[S::BPT];
+        widen<T, S::BPT>(r, v);
+#pragma unroll
+        for (int e = 0; e < S::BPT; ++e) v[e] = inb ? v[e] : 0.f;
+        const int at = part.bt * S::N + part.bn;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            if constexpr (S::BPT % 4 == 0) {
+#pragma unroll
+                for (int e = 0; e < S::BPT; e += 4)
+                    *reinterpret_cast<float4 *>(&to[k][at + e]) = make_float4(v[e ^ k], v[(e + 1) ^ k], v[(e + 2) ^ k], v[(e + 3) ^ k]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < S::BPT; ++e) to[k][(at + e) ^ k] = v[e];
+            }
+        }
+    };
+    const auto put_tile = [&](bool in, float (&x)[S::EPT], float (&d)[S::EPT]) {
 #pragma unroll
         for (int e = 0; e < S::EPT; ++e) {
-            const float v = to_f32(rd.e[e]) + bias[e];
-            const float d = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
-            sm.sdd[pt][pc + e] = d;
-            sm.sdx[pt][pc + e] = d * to_f32(rx.e[e]);
+            d[e] += bias[e];
+            d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+            x[e] = in ? d[e] * x[e] : 0.f;
         }
-#pragma unroll
-        for (int e = 0; e < S::BPT; ++e) sm.sb[bt][bn + e] = to_f32(rb.e[e]);
+        put_steps<S>(sm.sd, pt, pc, d, x);
+    };
+    const float4 *d0 = &sm.sd[0][S::column(cl, 0)], *d1 = &sm.sd[0][S::column(cl, 1)];
+    const float2 *g0 = &sm.sg[0][S::column(cl, 0)], *g1 = &sm.sg[0][S::column(cl, 1)];
+    const float *lb = &sm.sb[ox][n0], *lc = &sm.sc[ox][n0];
+
+    if (tiles) load(w.t0, false);
+    for (int i = 0; i < tiles; ++i) {
+        const int t = w.t0 + i * TC;
+        float x[S::EPT], d[S::EPT];
+        widen<T, S::EPT>(rx, x);
+        widen<T, S::EPT>(rd, d);
+        put_tile(t + pt < end, x, d);
+        put_bc(sm.sb, rb, t + part.bt < end);
         __syncthreads();
-        if (i + 1 < tiles) load_fwd(t + TC);
+        if (i + 1 < tiles) load(t + TC, false);
 #pragma unroll 1
         for (int s = 0; s < TC; s += kSub) {
-            put((i * TC + s) / kSub, h);
+            store_pairs<NP>(ck + (long long)((i * TC + s) / kSub) * kThreads * NS, h);
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
-                const float d = sm.sdd[s + u][cl], v = sm.sdx[s + u][cl];
+                const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
+                const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w);
+                f32x2 b[NP];
+                load_pairs<NP>(lb + (s + u) * S::N, b);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = fmaf(ex2(d * A2[j]), h[j], v * sm.sb[s + u][n0 + j]);
+                for (int j = 0; j < NP; ++j) h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
             }
         }
         __syncthreads();
@@ -459,174 +607,206 @@ template <typename T, typename S> __global__ void __launch_bounds__(kThreads) sc
 
     // the adjoint that enters at the segment's end
     if (on) {
-        if (a.dh_L)
-#pragma unroll
-            for (int j = 0; j < NS; ++j) p[j] = a.dh_L[bc * S::N + n0 + j];
+        if (a.dh_L) gather<S>(a.dh_L + bc * S::N + n0, ox, p);
         const long long stride = (long long)a.B * a.C;
         for (int s = a.nseg - 1; s > w.seg; --s) {
             const float d = a.seg_d[s * stride + bc];
+            f32x2 own[NP];
+            gather<S>(a.seg_p + (s * stride + bc) * S::N + n0, ox, own);
 #pragma unroll
-            for (int j = 0; j < NS; ++j) p[j] = fmaf(ex2(d * A2[j]), p[j], a.seg_p[(s * stride + bc) * S::N + n0 + j]);
+            for (int j = 0; j < NP; ++j) p[j] = fma2(ex2_2(mul2(pack2(d, d), A2[j])), p[j], own[j]);
         }
     }
-    const auto load_bwd = [&](int t) {
-        const long long row = (long long)w.b * a.L + t + pt, rowb = (long long)w.b * a.L + t + bt;
-        const bool in = t + pt < end, inb = t + bt < end;
-        rx = load_row<T, S::EPT>(a.x, a.ldx, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rd = load_row<T, S::EPT>(a.dt, a.lddt, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        ry = load_row<T, S::EPT>(a.dy, a.C, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        if (a.z) rz = load_row<T, S::EPT>(a.z, a.ldz, row, w.c0 + pc, w.nc - pc, in, a.vec);
-        rb = load_bc<T, S>(a.Bm, a.ldb, rowb, w.g * S::N + bn, inb, a.vec);
-        rc = load_bc<T, S>(a.Cm, a.ldc, rowb, w.g * S::N + bn, inb, a.vec);
-    };
     const int all = (w.t1 - w.t0 + TC - 1) / TC;  // tiles with padding: their outputs are zeros
-    if (tiles) load_bwd(w.t0 + (tiles - 1) * TC);
+    if (tiles) load(w.t0 + (tiles - 1) * TC, true);
     for (int i = all - 1; i >= 0; --i) {
         const int t = w.t0 + i * TC;
         const bool in = t + pt < end;
         const Raw<T, S::EPT> cx = rx, cd = rd, cz = rz, cy = ry;
+        float d[S::EPT], g[S::EPT];
+#pragma unroll
+        for (int e = 0; e < S::EPT; ++e) d[e] = g[e] = 0.f;
         if (i < tiles) {
+            float x[S::EPT], z[S::EPT];
+            widen<T, S::EPT>(rx, x);
+            widen<T, S::EPT>(rd, d);
+            widen<T, S::EPT>(ry, g);
+            widen<T, S::EPT>(rz, z);
+            put_tile(in, x, d);
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                const float v = to_f32(rd.e[e]) + bias[e];
-                const float d = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
-                const float y = to_f32(ry.e[e]);
-                sm.sdd[pt][pc + e] = d;
-                sm.sdx[pt][pc + e] = d * to_f32(rx.e[e]);
-                sm.sg[pt][pc + e] = a.z ? y * silu_f32(to_f32(rz.e[e])) : y;
+                if (a.z) g[e] *= silu_f32(z[e]);
+                g[e] = in ? g[e] : 0.f;
+                sm.sg[pt][S::column(pc + e, pt)] = make_float2(g[e], g[e]);
             }
-#pragma unroll
-            for (int e = 0; e < S::BPT; ++e) {
-                sm.sb[bt][bn + e] = to_f32(rb.e[e]);
-                sm.sc[bt][bn + e] = to_f32(rc.e[e]);
-            }
+            put_bc(sm.sb, rb, t + part.bt < end);
+            put_bc(sm.sc, rc, t + part.bt < end);
             __syncthreads();
-            if (i > 0) load_bwd(t - TC);
+            if (i > 0) load(t - TC, true);
+            f32x2 next[NP];
+            load_pairs<NP>(ck + (long long)((i * TC + TC - kSub) / kSub) * kThreads * NS, next);
 #pragma unroll 1
             for (int s = TC - kSub; s >= 0; s -= kSub) {
-                float hs[kSub + 1][NS], es[kSub][NS];
-                widen<float, NS>(load_raw<float, NS>(ck + (long long)((i * TC + s) / kSub) * kThreads * NS), hs[0]);
+                f32x2 hs[kSub + 1][NP], es[kSub][NP], part_dA[NP];
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    hs[0][j] = next[j];
+                    part_dA[j] = 0ull;
+                }
+                if (s > 0) load_pairs<NP>(ck + (long long)((i * TC + s) / kSub - 1) * kThreads * NS, next);
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
-                    const float d = sm.sdd[s + u][cl], v = sm.sdx[s + u][cl];
+                    const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
+                    const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w);
+                    f32x2 b[NP];
+                    load_pairs<NP>(lb + (s + u) * S::N, b);
 #pragma unroll
-                    for (int j = 0; j < NS; ++j) {
-                        es[u][j] = ex2(d * A2[j]);
-                        hs[u + 1][j] = fmaf(es[u][j], hs[u][j], v * sm.sb[s + u][n0 + j]);
+                    for (int j = 0; j < NP; ++j) {
+                        es[u][j] = ex2_2(mul2(dd, A2[j]));
+                        hs[u + 1][j] = fma2(es[u][j], hs[u][j], mul2(uu, b[j]));
                     }
                 }
 #pragma unroll
-                for (int u0 = kSub - S::TB; u0 >= 0; u0 -= S::TB) {
-                    float q1[S::TB], q2[S::TB], q3[S::TB];
+                for (int u0 = kSub - TB; u0 >= 0; u0 -= TB) {
+                    float q1[TB], q2[TB], q3[TB];
 #pragma unroll
-                    for (int uu = S::TB - 1; uu >= 0; --uu) {
-                        const int u = u0 + uu;
-                        const float d = sm.sdd[s + u][cl], v = sm.sdx[s + u][cl], g = sm.sg[s + u][cl];
-                        float m[2 * NS];  // dB, dC
-                        q1[uu] = q2[uu] = q3[uu] = 0.f;
+                    for (int uu0 = TB - 1; uu0 >= 0; --uu0) {
+                        const int u = u0 + uu0;
+                        const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
+                        const float2 gv = (u & 1 ? g1 : g0)[(s + u) * S::CT];
+                        const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w), gg = pack2(gv.x, gv.y);
+                        f32x2 b[NP], q[NP], y1 = 0ull, y2 = 0ull, y3 = 0ull;
+                        load_pairs<NP>(lb + (s + u) * S::N, b);
+                        load_pairs<NP>(lc + (s + u) * S::N, q);
+                        float m[2 * NS];  // for each register j: dB, dC
 #pragma unroll
-                        for (int j = 0; j < NS; ++j) {
-                            const float cc = sm.sc[s + u][n0 + j];
-                            p[j] = fmaf(cc, g, p[j]);
-                            m[j] = p[j] * v;
-                            m[NS + j] = hs[u + 1][j] * g;
-                            q1[uu] = fmaf(p[j], sm.sb[s + u][n0 + j], q1[uu]);
-                            q3[uu] = fmaf(hs[u + 1][j], cc, q3[uu]);
-                            p[j] *= es[u][j];
-                            const float q = p[j] * hs[u][j];
-                            q2[uu] = fmaf(q, A1[j], q2[uu]);
-                            dA[j] = fmaf(q, d, dA[j]);
-                            if (!on) m[j] = m[NS + j] = 0.f;  // no channel: 0 even beside an infinite B or C
+                        for (int j = 0; j < NP; ++j) {
+                            p[j] = fma2(q[j], gg, p[j]);
+                            const float2 mb = unpack2(mul2(p[j], uu)), mc = unpack2(mul2(hs[u + 1][j], gg));
+                            m[4 * j] = on ? mb.x : 0.f;  // no channel: 0 even beside an infinite B or C
+                            m[4 * j + 1] = on ? mc.x : 0.f;
+                            m[4 * j + 2] = on ? mb.y : 0.f;
+                            m[4 * j + 3] = on ? mc.y : 0.f;
+                            y1 = j ? fma2(p[j], b[j], y1) : mul2(p[j], b[j]);
+                            y3 = j ? fma2(hs[u + 1][j], q[j], y3) : mul2(hs[u + 1][j], q[j]);
+                            p[j] = mul2(p[j], es[u][j]);
+                            const f32x2 r = mul2(p[j], hs[u][j]);
+                            y2 = j ? fma2(r, A1[j], y2) : mul2(r, A1[j]);
+                            part_dA[j] = fma2(r, dd, part_dA[j]);
                         }
-                        halve<2 * NS, LN, 32>(m, lane);
-                        constexpr int left = 2 * NS > S::LC ? 2 * NS / S::LC : 1;
-                        const int first = halved_index<2 * NS, LN, 32>(lane);
+                        q1[uu0] = sum2(y1);
+                        q2[uu0] = sum2(y2);
+                        q3[uu0] = sum2(y3);
+                        // over the channel lanes: first the state bits, by the lanes' orders, then dB from dC
+                        constexpr int SB = NS == 4 ? (S::LC >= 4 ? 2 : 1) : 1;  // state bits that are halved
+                        constexpr int V1 = 2 * NS >> SB, ST = LN << SB;
+                        if constexpr (SB == 2) {
 #pragma unroll
-                        for (int k = 0; k < left; ++k)
-                            sm.bc[warp][s + u][(first + k) / NS][n0 + (first + k) % NS] = m[k];
+                            for (int k = 0; k < NS; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS], LN);
+#pragma unroll
+                            for (int k = 0; k < NS / 2; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS / 2], 2 * LN);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < NS; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS], LN);
+                        }
+                        // left: V1 / 2 states (registers 0 ..), dB and dC of each
+                        if constexpr (ST < 32) {
+                            static_assert(V1 == 2, "one state is left where lanes are");
+                            halve<2, ST, 32>(m, lane);
+                            sm.bc[warp][s + u][(lane & ST) ? 1 : 0][n0 + ox] = m[0];
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < V1; ++k) sm.bc[warp][s + u][k & 1][n0 + ((k >> 1) ^ ox)] = m[k];
+                        }
                     }
-                    halve<S::TB, 1, LN>(q1, lane);
-                    halve<S::TB, 1, LN>(q2, lane);
-                    if (a.z) halve<S::TB, 1, LN>(q3, lane);
-                    if (LN <= S::TB || ln < S::TB) {
-                        const int tt = s + u0 + halved_index<S::TB, 1, LN>(lane);
+                    halve<TB, 1, LN>(q1, lane);
+                    halve<TB, 1, LN>(q2, lane);
+                    if (a.z) halve<TB, 1, LN>(q3, lane);
+                    if (LN <= TB || ln < TB) {
+                        const int tt = s + u0 + halved_index<TB, 1, LN>(lane);
                         sm.s1[tt][cl] = q1[0];
                         sm.s2[tt][cl] = q2[0];
                         sm.s3[tt][cl] = q3[0];
                     }
                 }
+                // the long sum over tokens, with what its additions lose carried on
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const f32x2 add = add2(part_dA[j], lost[j]), to = add2(dA[j], add);
+                    lost[j] = add2(add, fma2(to, minus, dA[j]));
+                    dA[j] = to;
+                }
             }
             __syncthreads();
         }
         if (t + pt < w.t1 && pc < w.nc) {
-            float ox[S::EPT], od[S::EPT], oz[S::EPT];
+            float x[S::EPT], v[S::EPT], y[S::EPT], z[S::EPT], q1[S::EPT], q2[S::EPT], q3[S::EPT];
+            widen<T, S::EPT>(cx, x);
+            widen<T, S::EPT>(cd, v);
+            widen<T, S::EPT>(cy, y);
+            widen<T, S::EPT>(cz, z);
+            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s1[pt][pc]), q1);
+            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s2[pt][pc]), q2);
+            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s3[pt][pc]), q3);
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                ox[e] = od[e] = oz[e] = 0.f;
-                if (!in) continue;
-                const float x = to_f32(cx.e[e]), v = to_f32(cd.e[e]) + bias[e];
-                const float d = sm.sdd[pt][pc + e], g = sm.sg[pt][pc + e], q1 = sm.s1[pt][pc + e];
-                ox[e] = fmaf(d, q1, dskip[e] * g);
-                od[e] = fmaf(x, q1, sm.s2[pt][pc + e]);
-                if (a.softplus) {
-                    const float ev = __expf(-fabsf(v));
-                    od[e] *= __fdividef(v >= 0.f ? 1.f : ev, 1.f + ev);
-                }
-                ab[e] += od[e];
-                aD[e] = fmaf(g, x, aD[e]);
-                if (a.z)
-                    oz[e] = to_f32(cy.e[e]) * fmaf(dskip[e], x, sm.s3[pt][pc + e]) * dsilu_f32(to_f32(cz.e[e]));
+                q2[e] = fmaf(x[e], q1[e], q2[e]);
+                if (a.softplus) q2[e] *= sigmoid_f32(v[e] + bias[e]);
+                q1[e] = fmaf(d[e], q1[e], dskip[e] * g[e]);
+                if (a.z) z[e] = y[e] * fmaf(dskip[e], x[e], q3[e]) * dsilu_f32(z[e]);
+                q1[e] = in ? q1[e] : 0.f;
+                q2[e] = in ? q2[e] : 0.f;
+                z[e] = in ? z[e] : 0.f;
+                ab[e] += q2[e];
+                aD[e] += in ? g[e] * x[e] : 0.f;
             }
             const long long at = ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
-            T *o[3] = {static_cast<T *>(a.dx) + at, static_cast<T *>(a.ddt) + at, a.z ? static_cast<T *>(a.dz) + at : nullptr};
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                if (!o[k]) continue;
-                const Raw<T, S::EPT> r = narrow<T, S::EPT>(k == 0 ? ox : k == 1 ? od : oz);
-                if (a.vec) store_raw<T, S::EPT>(o[k], r);
-                else store_raw_any<T, S::EPT>(o[k], r, w.nc - pc);
-            }
+            const auto put = [&](void *to, const float (&o)[S::EPT]) {
+                const Raw<T, S::EPT> r = narrow<T, S::EPT>(o);
+                if constexpr (VEC) store_raw<T, S::EPT>(static_cast<T *>(to) + at, r);
+                else store_raw_any<T, S::EPT>(static_cast<T *>(to) + at, r, w.nc - pc);
+            };
+            put(a.dx, q1);
+            put(a.ddt, q2);
+            if (a.z) put(a.dz, z);
         }
         // the block's share of dB and dC
-        for (int k = tid; k < TC * 2 * S::N; k += kThreads) {
+        for (int k = tid * 4; k < TC * 2 * S::N; k += kThreads * 4) {
             const int tt = k / (2 * S::N), r = k % (2 * S::N);
             if (t + tt >= w.t1) break;
-            float v = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t + tt < end)
 #pragma unroll
-                for (int u = 0; u < kThreads / 32; ++u) v += (&sm.bc[u][tt][0][0])[r];
-            a.part_bc[((((long long)w.tile * a.B + w.b) * a.L + t + tt) * a.G + w.g) * (2 * S::N) + r] = v;
+                for (int u = 0; u < kThreads / 32; ++u) {
+                    const float4 o = *reinterpret_cast<const float4 *>(&sm.bc[u][tt][0][0] + r);
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+            *reinterpret_cast<float4 *>(a.part_bc + ((((long long)w.tile * a.B + w.b) * a.L + t + tt) * a.G + w.g) * (2 * S::N) + r) = v;
         }
         __syncthreads();
     }
 
-    float *part = a.part + (long long)(w.seg * a.B + w.b) * a.C * (S::N + 2);
+    float *sums = a.part + (long long)(w.seg * a.B + w.b) * a.C * (S::N + 2);
     if (on) {
-        if (w.seg == 0 && a.dh0)
-#pragma unroll
-            for (int j = 0; j < NS; ++j) a.dh0[bc * S::N + n0 + j] = p[j];
-        float *pa = part + (long long)c * S::N + n0;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) pa[j] = dA[j];
+        if (w.seg == 0 && a.dh0) scatter<S>(a.dh0 + bc * S::N + n0, ox, p);
+        scatter<S>(sums + (long long)c * S::N + n0, ox, dA);
     }
     // dD and ddt_bias: over the tokens that each thread prepared
-    float *red = &sm.s1[0][0], *red2 = &sm.s2[0][0];
 #pragma unroll
     for (int e = 0; e < S::EPT; ++e) {
-        red[pt * (S::CT + S::PAD) + pc + e] = aD[e];
-        red2[pt * (S::CT + S::PAD) + pc + e] = ab[e];
+        sm.s1[pt][pc + e] = aD[e];
+        sm.s2[pt][pc + e] = ab[e];
     }
     __syncthreads();
-    for (int k = tid; k < S::CT; k += kThreads)
-        if (k < w.nc) {
-            float u = 0.f, v = 0.f;
-            for (int tt = 0; tt < TC; ++tt) {
-                u += sm.s1[tt][k];
-                v += sm.s2[tt][k];
-            }
-            part[(long long)a.C * S::N + w.c0 + k] = u;
-            part[(long long)a.C * (S::N + 1) + w.c0 + k] = v;
+    if (tid < w.nc) {
+        float u = 0.f, v = 0.f;
+        for (int tt = 0; tt < TC; ++tt) {
+            u += sm.s1[tt][tid];
+            v += sm.s2[tt][tid];
         }
+        sums[(long long)a.C * S::N + w.c0 + tid] = u;
+        sums[(long long)a.C * (S::N + 1) + w.c0 + tid] = v;
+    }
 }
 
 // dB and dC from the blocks' shares: part[tile][rows][G][2][N] over the tiles of a group.

@@ -2,6 +2,8 @@
 // rounded from fp32, for the kernels whose rows may be strided, odd or not
 // aligned for 16-byte accesses.
 #pragma once
+#include <string.h>
+
 #include "efla_common.cuh"
 
 namespace efla {
@@ -27,14 +29,33 @@ template <typename T, int N> __device__ __forceinline__ Raw<T, N> zero_raw() {
     for (int i = 0; i < N; ++i) r.e[i] = from_f32<T>(0.f);
     return r;
 }
+// bf16 is widened and rounded by pairs: one shift or mask, and half a
+// conversion, an element.
 template <typename T, int N> __device__ __forceinline__ void widen(const Raw<T, N> &r, float (&v)[N]) {
+    if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+        uint32_t u[N / 2];
+        memcpy(u, r.e, sizeof(u));
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32(r.e[i]);
+        for (int i = 0; i < N / 2; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f32(r.e[i]);
+    }
 }
 template <typename T, int N> __device__ __forceinline__ Raw<T, N> narrow(const float (&v)[N]) {
     Raw<T, N> r;
+    if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+        __nv_bfloat162 p[N / 2];
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.e[i] = from_f32<T>(v[i]);
+        for (int i = 0; i < N / 2; ++i) p[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        memcpy(r.e, p, sizeof(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.e[i] = from_f32<T>(v[i]);
+    }
     return r;
 }
 template <typename T, int N> __device__ __forceinline__ void store_raw(T *p, const Raw<T, N> &r) {
@@ -46,15 +67,61 @@ template <typename T, int N> __device__ __forceinline__ void store_raw_any(T *p,
         if (i < n) p[i] = r.e[i];
 }
 
-// 1 / (1 + e^-v) and v / (1 + e^-v).  The division is the approximate one
-// (2 ulp); for v below -87 its result is 0 instead of a value under 2^-120.
-__device__ __forceinline__ float sigmoid_f32(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-__device__ __forceinline__ float silu_f32(float v) { return __fdividef(v, 1.f + __expf(-v)); }
-// d silu(v) / dv = s (1 + v (1 - s)), s = sigmoid(v); 1 - s as e^-v s.
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 2^v and 1 / v, approximate (2 and 1 ulp); subnormals count as zeros.
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + e^-v) and v / (1 + e^-v); where e^-v overflows they are 0 and -0.
+__device__ __forceinline__ float sigmoid_f32(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
+__device__ __forceinline__ float silu_f32(float v) { return v * sigmoid_f32(v); }
+// silu and its derivative s (1 + v (1 - s)), s = sigmoid(v), with 1 - s as
+// e^-v s.  Below -80 the derivative is under 2^-100 and given as 0, where
+// e^-v times 0 would be no number.
 __device__ __forceinline__ float dsilu_f32(float v) {
-    const float e = __expf(-v);
-    const float s = __fdividef(1.f, 1.f + e);
+    const float e = ex2(-kLog2e * v), s = rcp(1.f + e);
     return v < -80.f ? 0.f : s * fmaf(v * e, s, 1.f);
+}
+
+// Two fp32 operations in one instruction, on a register pair.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return t.x + t.y;
 }
 
 // Column sums of partial results, in a fixed order: out[i] = sum_p part[p][i].
