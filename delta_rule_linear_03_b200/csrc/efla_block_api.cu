@@ -270,7 +270,9 @@ template <typename T, typename S, bool VEC> efla_status_t run_scan_fwd(const sca
         scan::segment_kernel<T, S, VEC, false><<<grid, scan::kThreads, 0, st>>>(a);
         if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
     }
-    scan::scan_fwd_kernel<T, S, VEC><<<grid, scan::kThreads, 0, st>>>(a);
+    constexpr size_t smem = sizeof(scan::FwdSmem<S>);
+    if (!ensure_smem<scan::scan_fwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
+    scan::scan_fwd_kernel<T, S, VEC><<<grid, 2 * scan::kThreads, smem, st>>>(a);
     return launched();
 }
 

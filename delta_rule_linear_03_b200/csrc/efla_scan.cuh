@@ -85,28 +85,52 @@ template <int N_, int NS_> struct Shape {
     }
 };
 
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return pack2(ex2(t.x), ex2(t.y));
+}
+__device__ __forceinline__ f32x2 rcp_2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return pack2(rcp(t.x), rcp(t.y));
+}
+__device__ __forceinline__ f32x2 twice(float v) { return pack2(v, v); }
+
 // softplus(v) = max(v, 0) + log1p(e), e = e^-|v|, by log1p(e) = 2 atanh(s),
 // s = e / (2 + e) <= 1/3, whose series s + s^3/3 + ... + s^13/13 leaves less
 // than 2^-26 of it.  A step's error goes into every decay of its token, so e
 // and s are taken to the last bits: what the argument's product with log2 e
-// loses is put back to first order, and the quotient has one Newton step.
-__device__ __forceinline__ float softplus_f32(float v) {
-    const float a = fabsf(v) > 126.f ? -126.f : -fabsf(v), t = a * kLog2e;  // e is 0 from there on; NaN stays
-    const float lo = fmaf(a, 1.925963e-8f, fmaf(a, kLog2e, -t));              // the rounding of log2 e, that of the product
-    float e = ex2(t);
-    e = fmaf(e * lo, 0.6931472f, e);
-    const float w = 2.f + e, r = rcp(w);
-    float s = e * r;
-    s = fmaf(fmaf(-s, w, e), r, s);
-    const float q = s * s;
-    float p = 1.f / 13.f;
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    const float s2 = s + s;
-    return fmaxf(v, 0.f) + fmaf(p * q, s2, s2);
+// and the rounding of log2 e lose is put back to first order, and the
+// quotient has one Newton step.  Two values at once.
+__device__ __forceinline__ f32x2 softplus_2(f32x2 v2) {
+    const float2 v = unpack2(v2);
+    const f32x2 a = pack2(fminf(fabsf(v.x), 126.f), fminf(fabsf(v.y), 126.f));  // e is 0 from there on
+    const f32x2 t = mul2(a, twice(-kLog2e));
+    const f32x2 lo = fma2(a, twice(-1.925963e-8f), fma2(a, twice(-kLog2e), mul2(a, twice(kLog2e))));
+    f32x2 e = ex2_2(t);
+    e = fma2(mul2(e, lo), twice(0.6931472f), e);
+    const f32x2 w = fma2(e, twice(-1.f), twice(-2.f)), r = rcp_2(w);  // -(2 + e)
+    f32x2 s = mul2(mul2(e, twice(-1.f)), r);
+    s = fma2(fma2(s, w, e), mul2(r, twice(-1.f)), s);
+    const f32x2 q = mul2(s, s);
+    f32x2 p = fma2(twice(1.f / 13.f), q, twice(1.f / 11.f));
+    p = fma2(p, q, twice(1.f / 9.f));
+    p = fma2(p, q, twice(1.f / 7.f));
+    p = fma2(p, q, twice(1.f / 5.f));
+    p = fma2(p, q, twice(1.f / 3.f));
+    const f32x2 s2 = add2(s, s);
+    float2 top;  // max(v, 0), a NaN stays one
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top.x) : "f"(v.x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top.y) : "f"(v.y));
+    return add2(pack2(top.x, top.y), fma2(mul2(p, q), s2, s2));
+}
+__device__ __forceinline__ float softplus_f32(float v) { return unpack2(softplus_2(twice(v))).x; }
+template <int N> __device__ __forceinline__ void softplus_all(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 t = unpack2(softplus_2(pack2(v[i], v[i + 1])));
+        v[i] = t.x;
+        v[i + 1] = t.y;
+    }
 }
 
 // Sums v[0..V) over the 2^k lanes that differ in the bits of [STEP, LIM).
@@ -204,11 +228,6 @@ template <int NP> __device__ __forceinline__ void load_pairs(const float *p, f32
 template <int NP> __device__ __forceinline__ void store_pairs(float *p, const f32x2 (&v)[NP]) {
     if constexpr (NP == 2) *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v[0], v[1]);
     else *reinterpret_cast<f32x2 *>(p) = v[0];
-}
-
-__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
-    const float2 t = unpack2(v);
-    return pack2(ex2(t.x), ex2(t.y));
 }
 
 // Register j of a lane holds state n0 + (j ^ x); x is 0 but in the backward pass.
@@ -326,9 +345,11 @@ __global__ void __launch_bounds__(kThreads) segment_kernel(Args a) {
                     for (int e = 0; e < S::EPT; ++e) x[e] *= silu_f32(z[e]);
             }
 #pragma unroll
+            for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
+            if (a.softplus) softplus_all<S::EPT>(d);
+#pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                d[e] += bias[e];
-                d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+                d[e] = in ? d[e] : 0.f;
                 x[e] = in ? (REV ? x[e] : d[e] * x[e]) : 0.f;
             }
             put_steps<S>(sd, pt, pc, d, x);
@@ -361,114 +382,154 @@ __global__ void __launch_bounds__(kThreads) segment_kernel(Args a) {
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(Args a) {
-    __shared__ float4 sd[S::TC][S::CT];               // D, D, D x, D x
-    __shared__ __align__(16) float sy[S::TC][S::CS];  // <C, h>
-    __shared__ __align__(16) float sb[S::TC][S::N], sc[S::TC][S::N];
-    constexpr int NP = S::NP;
+// Four warps run the recurrence, four others prepare the next tile for them
+// and finish the one before: the preparation is two thirds as many
+// instructions as the recurrence, and beside it they cost no time of their
+// own.  Two buffers, one barrier a tile.
+template <typename S> struct FwdSmem {
+    float4 sd[2][S::TC][S::CT];               // D, D, D x, D x
+    alignas(16) float sy[2][S::TC][S::CS];    // <C, h>
+    alignas(16) float sb[2][S::TC][S::N], sc[2][S::TC][S::N];
+};
+
+__device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 * kThreads) scan_fwd_kernel(Args a) {
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(raw_smem);
+    constexpr int NP = S::NP, TC = S::TC, TB = S::TB;
     const Where w(a, S::CT);
-    const Part<T, S> part(threadIdx.x);
-    const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
-    const int c = w.c0 + cl, n0 = ln * S::NS, pt = part.pt, pc = part.pc;
-    const bool on = cl < w.nc;
-    f32x2 A2[NP], h[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
-    if (on) gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], pack2(kLog2e, kLog2e));
-    if (on) start_state<S>(a, w, c, n0, 0, A2, h);
     const int end = min(w.t1, w.len);
-    float bias[S::EPT], dskip[S::EPT];
+    const int all = (w.t1 - w.t0 + TC - 1) / TC;                           // tiles
+    const int tiles = end > w.t0 ? (end - w.t0 + TC - 1) / TC : 0;         // those with tokens that count
+    if (threadIdx.x < kThreads) {  // the recurrence
+        const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
+        const int c = w.c0 + cl, n0 = ln * S::NS;
+        const bool on = cl < w.nc;
+        f32x2 A2[NP], h[NP];
 #pragma unroll
-    for (int i = 0; i < S::EPT; ++i) {
-        bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
-        dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
-    }
-    const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
-    const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
-    const long long ldz = a.z ? a.ldz : a.ldx;
-    const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
-    Raw<T, S::EPT> rx, rd, rz;
-    Raw<T, S::BPT> rb, rc;
-    const auto load = [&](int t) {
-        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
-        rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
-        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-        rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-        rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
-        rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
-    };
-    load(w.t0);
-    const float4 *d0 = &sd[0][S::column(cl, 0)], *d1 = &sd[0][S::column(cl, 1)];
-    float *out = &sy[halved_index<S::TB, 1, S::LN>(lane)][cl];
-    for (int t = w.t0; t < w.t1; t += S::TC) {
-        const Raw<T, S::EPT> cx = rx, cz = rz;
-        const bool in = t + pt < end;
-        {
-            const bool inb = t + part.bt < end;
+        for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
+        if (on) gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], twice(kLog2e));
+        if (on) start_state<S>(a, w, c, n0, 0, A2, h);
+        const int k0 = S::column(cl, 0), k1 = S::column(cl, 1), o = halved_index<TB, 1, S::LN>(lane) * S::CS + cl;
+        tile_barrier();
+        for (int k = 0; k < all; ++k) {
+            const int f = k & 1;
+            const float4 *d0 = &sm.sd[f][0][k0], *d1 = &sm.sd[f][0][k1];
+            const float *sb = &sm.sb[f][0][n0], *sc = &sm.sc[f][0][n0];
+            float *out = &sm.sy[f][0][0] + o;
+            if (k < tiles) {
+#pragma unroll 2
+                for (int s = 0; s < TC; s += TB) {
+                    float p[TB];
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        const float4 d = (u & 1 ? d1 : d0)[(s + u) * S::CT];
+                        const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
+                        f32x2 b[NP], q[NP], y = 0ull;
+                        load_pairs<NP>(sb + (s + u) * S::N, b);
+                        load_pairs<NP>(sc + (s + u) * S::N, q);
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) {
+                            h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
+                            y = j ? fma2(h[j], q[j], y) : mul2(h[j], q[j]);
+                        }
+                        p[u] = sum2(y);
+                    }
+                    halve<TB, 1, S::LN>(p, lane);
+                    if (S::LN <= TB || ln < TB) out[s * S::CS] = p[0];
+                }
+            }
+            tile_barrier();
+        }
+        if (a.h_L && on && w.seg == a.nseg - 1) scatter<S>(a.h_L + ((long long)w.b * a.C + c) * S::N + n0, 0, h);
+    } else {  // preparation and outputs
+        const Part<T, S> part(threadIdx.x - kThreads);
+        const int pt = part.pt, pc = part.pc;
+        float bias[S::EPT], dskip[S::EPT];
+#pragma unroll
+        for (int i = 0; i < S::EPT; ++i) {
+            bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
+            dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
+        }
+        const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
+        const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+        const long long ldz = a.z ? a.ldz : a.ldx;
+        const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
+        Raw<T, S::EPT> rx, rd, rz, mx, mz, ox, oz;  // of the tile that comes in, the one worked on, the one to finish
+        Raw<T, S::BPT> rb, rc;
+        const auto load = [&](int k) {
+            const int t = w.t0 + k * TC;
+            const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
+            rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
+            rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+            rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+            rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
+            rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+        };
+        const auto prepare = [&](int k) {
+            const int t = w.t0 + k * TC, f = k & 1;
+            const bool in = t + pt < end, inb = t + part.bt < end;
             float x[S::EPT], d[S::EPT], b[S::BPT], q[S::BPT];
             widen<T, S::EPT>(rx, x);
             widen<T, S::EPT>(rd, d);
             widen<T, S::BPT>(rb, b);
             widen<T, S::BPT>(rc, q);
 #pragma unroll
+            for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
+            if (a.softplus) softplus_all<S::EPT>(d);
+#pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                d[e] += bias[e];
-                d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+                d[e] = in ? d[e] : 0.f;
                 x[e] = in ? d[e] * x[e] : 0.f;
             }
-            put_steps<S>(sd, pt, pc, d, x);
+            put_steps<S>(sm.sd[f], pt, pc, d, x);
 #pragma unroll
             for (int e = 0; e < S::BPT; ++e) {
                 b[e] = inb ? b[e] : 0.f;
                 q[e] = inb ? q[e] : 0.f;
             }
-            store_raw<float, S::BPT>(&sb[part.bt][part.bn], narrow<float, S::BPT>(b));
-            store_raw<float, S::BPT>(&sc[part.bt][part.bn], narrow<float, S::BPT>(q));
-        }
-        __syncthreads();
-        if (t + S::TC < w.t1) load(t + S::TC);
-        if (t < end) {
-#pragma unroll 2
-            for (int s = 0; s < S::TC; s += S::TB) {
-                float p[S::TB];
-#pragma unroll
-                for (int u = 0; u < S::TB; ++u) {
-                    const float4 d = (u & 1 ? d1 : d0)[(s + u) * S::CT];
-                    const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
-                    f32x2 b[NP], q[NP], y = 0ull;
-                    load_pairs<NP>(&sb[s + u][n0], b);
-                    load_pairs<NP>(&sc[s + u][n0], q);
-#pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
-                        y = j ? fma2(h[j], q[j], y) : mul2(h[j], q[j]);
-                    }
-                    p[u] = sum2(y);
-                }
-                halve<S::TB, 1, S::LN>(p, lane);
-                if (S::LN <= S::TB || ln < S::TB) out[s * S::CS] = p[0];
-            }
-        }
-        __syncthreads();
-        if (t + pt < w.t1 && pc < w.nc) {
+            store_raw<float, S::BPT>(&sm.sb[f][part.bt][part.bn], narrow<float, S::BPT>(b));
+            store_raw<float, S::BPT>(&sm.sc[f][part.bt][part.bn], narrow<float, S::BPT>(q));
+        };
+        const auto finish = [&](int k) {
+            const int t = w.t0 + k * TC, f = k & 1;
+            if (t + pt >= w.t1 || pc >= w.nc) return;
             float x[S::EPT], z[S::EPT], o[S::EPT];
-            widen<T, S::EPT>(cx, x);
-            widen<T, S::EPT>(cz, z);
-            widen<float, S::EPT>(load_raw<float, S::EPT>(&sy[pt][pc]), o);
+            widen<T, S::EPT>(ox, x);
+            widen<T, S::EPT>(oz, z);
+            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.sy[f][pt][pc]), o);
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
                 o[e] = fmaf(dskip[e], x[e], o[e]);
                 if (a.z) o[e] *= silu_f32(z[e]);
-                o[e] = in ? o[e] : 0.f;
+                o[e] = t + pt < end ? o[e] : 0.f;
             }
             T *y = static_cast<T *>(a.y) + ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
             if constexpr (VEC) store_raw<T, S::EPT>(y, narrow<T, S::EPT>(o));
             else store_raw_any<T, S::EPT>(y, narrow<T, S::EPT>(o), w.nc - pc);
+        };
+        load(0);
+        prepare(0);
+        mx = rx;
+        mz = rz;
+        load(1);
+        tile_barrier();
+        for (int k = 0; k < all; ++k) {
+            prepare(k + 1);  // past the last tile: zeros that nothing reads
+            const Raw<T, S::EPT> nx = rx, nz = rz;
+            load(k + 2);
+            if (k > 0) finish(k - 1);
+            ox = mx;
+            oz = mz;
+            mx = nx;
+            mz = nz;
+            tile_barrier();
         }
+        finish(all - 1);
     }
-    if (a.h_L && on && w.seg == a.nseg - 1) scatter<S>(a.h_L + ((long long)w.b * a.C + c) * S::N + n0, 0, h);
 }
 
 // ---------------------------------------------------------------- backward
@@ -568,9 +629,11 @@ template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(kT
     };
     const auto put_tile = [&](bool in, float (&x)[S::EPT], float (&d)[S::EPT]) {
 #pragma unroll
+        for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
+        if (a.softplus) softplus_all<S::EPT>(d);
+#pragma unroll
         for (int e = 0; e < S::EPT; ++e) {
-            d[e] += bias[e];
-            d[e] = in ? (a.softplus ? softplus_f32(d[e]) : d[e]) : 0.f;
+            d[e] = in ? d[e] : 0.f;
             x[e] = in ? d[e] * x[e] : 0.f;
         }
         put_steps<S>(sm.sd, pt, pc, d, x);
