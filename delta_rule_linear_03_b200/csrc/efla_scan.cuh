@@ -394,7 +394,7 @@ template <typename S> struct FwdSmem {
 
 __device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 * kThreads) scan_fwd_kernel(Args a) {
+template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(raw_smem);
     constexpr int NP = S::NP, TC = S::TC, TB = S::TB;
@@ -421,20 +421,38 @@ template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 
             const float *sb = &sm.sb[f][0][n0], *sc = &sm.sc[f][0][n0];
             float *out = &sm.sy[f][0][0] + o;
             if (k < tiles) {
-#pragma unroll 2
-                for (int s = 0; s < TC; s += TB) {
-                    float p[TB];
+                // decays and terms of the next TB tokens are fetched and computed beside the chain of these
+                f32x2 e[2][TB][NP], v[2][TB][NP];
+                const auto terms = [&](int s, f32x2(&e)[TB][NP], f32x2(&v)[TB][NP]) {
 #pragma unroll
                     for (int u = 0; u < TB; ++u) {
                         const float4 d = (u & 1 ? d1 : d0)[(s + u) * S::CT];
                         const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
-                        f32x2 b[NP], q[NP], y = 0ull;
-                        load_pairs<NP>(sb + (s + u) * S::N, b);
-                        load_pairs<NP>(sc + (s + u) * S::N, q);
+                        load_pairs<NP>(sb + (s + u) * S::N, v[u]);
 #pragma unroll
                         for (int j = 0; j < NP; ++j) {
-                            h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
-                            y = j ? fma2(h[j], q[j], y) : mul2(h[j], q[j]);
+                            e[u][j] = ex2_2(mul2(dd, A2[j]));
+                            v[u][j] = mul2(uu, v[u][j]);
+                        }
+                    }
+                };
+                terms(0, e[0], v[0]);
+#pragma unroll
+                for (int s = 0; s < TC; s += TB) {
+                    constexpr int two = 2 * TB;
+                    const int g = s % two / TB;
+                    f32x2 q[TB][NP];
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) load_pairs<NP>(sc + (s + u) * S::N, q[u]);
+                    if (s + TB < TC) terms(s + TB, e[g ^ 1], v[g ^ 1]);
+                    float p[TB];
+#pragma unroll
+                    for (int u = 0; u < TB; ++u) {
+                        f32x2 y = 0ull;
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) {
+                            h[j] = fma2(e[g][u][j], h[j], v[g][u][j]);
+                            y = j ? fma2(h[j], q[u][j], y) : mul2(h[j], q[u][j]);
                         }
                         p[u] = sum2(y);
                     }
