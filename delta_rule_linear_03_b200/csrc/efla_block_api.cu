@@ -9,6 +9,7 @@
 using namespace efla;
 using namespace efla::host;
 
+#include <cstdlib>
 namespace {
 
 // One buffer of a call: where it is, how many bytes from its first to its last.
@@ -157,41 +158,47 @@ bool rows_in_vectors(const void *p, long long ld, int vec, size_t e) {
 // ---------------------------------------------------------------- scan
 
 struct ScanPlan {
-    int ns, nseg, seg, tpg;
+    int ns, cp;  // state values of a lane in each channel, channels of a lane
+    int nseg, seg, tpg;
     long long blocks;  // of one segment
+    int sub() const { return ns * cp >= 8 ? 4 : 8; }  // tokens from one checkpoint of the backward pass to the next
 };
 
-constexpr int tile_channels(int N, int ns) { return scan::kThreads * ns / N; }
+constexpr int tile_channels(int N, int ns, int cp) { return scan::kThreads * ns / N * cp; }
 
-// How the work is cut.  A block is four warps, so num_sms blocks give every
-// scheduler one warp; the chain over time needs little more than that to
-// keep the exponentials busy.  With fewer blocks than SMs, two state values
-// a lane instead of four double the warps for a few shuffles more; where
-// that is not enough and the sequence is long, it is cut into segments, which
-// repeats the exponentials once (twice in the backward pass) and therefore
-// wants at least a third of the SMs idle.
+// How the work is cut.  Wide blocks (two channels a lane, eight state values
+// in all but N = 8) read least shared memory a value and are taken where they
+// give most SMs one; else a lane has one channel and two values (four of 64),
+// which makes four times as many blocks.  Where that still leaves most SMs
+// without one and the sequence is long, it is cut into segments of wide
+// blocks, which repeats the exponentials once (twice in the backward pass).
 ScanPlan scan_plan(int B, int L, int C, int G, int N, bool bwd) {
     ScanPlan p;
     const int sms = num_sms(), cg = C / G;
-    const auto blocks = [&](int ns) { return (long long)B * G * ((cg + tile_channels(N, ns) - 1) / tile_channels(N, ns)); };
-    p.ns = 4;
+    const auto shape = [&](int kind) {
+        p.ns = N == 64 || (kind > 0 && !(N == 8 && kind == 2)) ? 4 : 2;
+        p.cp = kind == 2 ? 2 : 1;
+        const int ct = tile_channels(N, p.ns, p.cp);
+        p.tpg = (cg + ct - 1) / ct;
+        return p.blocks = (long long)B * G * p.tpg;
+    };
     p.nseg = 1;
-    if (blocks(4) < sms && N <= 32) p.ns = 2;
-    const long long nb = blocks(p.ns);
-    if (nb * 3 < sms * 2LL) {
-        const long long want = 4LL * sms / std::max<long long>(1, blocks(4)), most = L / 128;
-        if (std::min(want, most) >= 3) {
-            p.ns = 4;
-            p.nseg = (int)std::min<long long>(std::min(want, most), 64);
+    const long long wide = shape(2);
+    if (wide * 8 < sms * 5LL) {
+        if (shape(0) * 2 < sms) {
+            const long long want = 2LL * sms / std::max<long long>(1, wide), most = L / 128;
+            if (std::min(want, most) >= 3) {
+                shape(2);
+                p.nseg = (int)std::min<long long>(std::min(want, most), 64);
+            }
         }
     }
     (void)bwd;
+    if (getenv("T_WIDE")) shape(atoi(getenv("T_WIDE")));
+    if (getenv("T_SEG")) p.nseg = atoi(getenv("T_SEG"));
     const int seg = (L + p.nseg - 1) / p.nseg;
     p.seg = (seg + 31) / 32 * 32;  // 32: a multiple of every tile
     p.nseg = L > 0 ? (L + p.seg - 1) / p.seg : 1;
-    const int ct = tile_channels(N, p.ns);
-    p.tpg = (cg + ct - 1) / ct;
-    p.blocks = (long long)B * G * p.tpg;
     return p;
 }
 
@@ -223,7 +230,7 @@ struct BwdSizes {
 BwdSizes bwd_sizes(const ScanPlan &p, int B, int L, int C, int G, int N) {
     BwdSizes s;
     s.seg = seg_floats(p, B, C, N, true);
-    s.ckpt = (size_t)p.blocks * p.nseg * (p.seg / scan::kSub) * scan::kThreads * p.ns;
+    s.ckpt = (size_t)p.blocks * p.nseg * (p.seg / p.sub()) * scan::kThreads * p.ns * p.cp;
     s.bc = (size_t)p.tpg * B * L * G * 2 * N;
     s.part = (size_t)p.nseg * B * C * (N + 2);
     return s;
@@ -241,17 +248,23 @@ efla_status_t check_scan(efla_dtype_t dtype, int B, int L, int C, int G, int N) 
     return EFLA_OK;
 }
 
-#define EFLA_SCAN_N(F, T, N, NS, ...)                                                          \
+#define EFLA_SCAN_N(F, T, N, P, ...)                                                           \
     do {                                                                                       \
-        if ((NS) == 4) {                                                                       \
-            if ((N) == 8) return F<T, scan::Shape<8, 4>>(__VA_ARGS__);                         \
-            if ((N) == 16) return F<T, scan::Shape<16, 4>>(__VA_ARGS__);                       \
-            if ((N) == 32) return F<T, scan::Shape<32, 4>>(__VA_ARGS__);                       \
-            return F<T, scan::Shape<64, 4>>(__VA_ARGS__);                                      \
+        if ((P).cp == 2) {                                                                     \
+            if ((N) == 8) return F<T, scan::Shape<8, 2, 2>>(__VA_ARGS__);                      \
+            if ((N) == 16) return F<T, scan::Shape<16, 4, 2>>(__VA_ARGS__);                    \
+            if ((N) == 32) return F<T, scan::Shape<32, 4, 2>>(__VA_ARGS__);                    \
+            return F<T, scan::Shape<64, 4, 2>>(__VA_ARGS__);                                   \
         }                                                                                      \
-        if ((N) == 8) return F<T, scan::Shape<8, 2>>(__VA_ARGS__);                             \
-        if ((N) == 16) return F<T, scan::Shape<16, 2>>(__VA_ARGS__);                           \
-        return F<T, scan::Shape<32, 2>>(__VA_ARGS__);                                          \
+        if ((P).ns == 4) {                                                                     \
+            if ((N) == 8) return F<T, scan::Shape<8, 4, 1>>(__VA_ARGS__);                      \
+            if ((N) == 16) return F<T, scan::Shape<16, 4, 1>>(__VA_ARGS__);                    \
+            if ((N) == 32) return F<T, scan::Shape<32, 4, 1>>(__VA_ARGS__);                    \
+            return F<T, scan::Shape<64, 4, 1>>(__VA_ARGS__);                                   \
+        }                                                                                      \
+        if ((N) == 8) return F<T, scan::Shape<8, 2, 1>>(__VA_ARGS__);                          \
+        if ((N) == 16) return F<T, scan::Shape<16, 2, 1>>(__VA_ARGS__);                        \
+        return F<T, scan::Shape<32, 2, 1>>(__VA_ARGS__);                                       \
     } while (0)
 
 template <typename T, typename S> bool scan_vec(const scan::Args &a) {
@@ -265,15 +278,20 @@ template <typename T, typename S> bool scan_vec(const scan::Args &a) {
     return v;
 }
 
+template <typename T, typename S, bool VEC, scan::Mode MODE>
+efla_status_t run_scan(const scan::Args &a, unsigned grid, cudaStream_t st) {
+    constexpr size_t smem = sizeof(scan::FwdSmem<S>);
+    if (!ensure_smem<scan::scan_fwd_kernel<T, S, VEC, MODE>>(smem)) return EFLA_ERR_CUDA;
+    scan::scan_fwd_kernel<T, S, VEC, MODE><<<grid, 2 * scan::kThreads, smem, st>>>(a);
+    return launched();
+}
+
 template <typename T, typename S, bool VEC> efla_status_t run_scan_fwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
     if (a.nseg > 1) {
-        scan::segment_kernel<T, S, VEC, false><<<grid, scan::kThreads, 0, st>>>(a);
-        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
+        const efla_status_t s = run_scan<T, S, VEC, scan::STATE>(a, grid, st);
+        if (s != EFLA_OK) return s;
     }
-    constexpr size_t smem = sizeof(scan::FwdSmem<S>);
-    if (!ensure_smem<scan::scan_fwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
-    scan::scan_fwd_kernel<T, S, VEC><<<grid, 2 * scan::kThreads, smem, st>>>(a);
-    return launched();
+    return run_scan<T, S, VEC, scan::FULL>(a, grid, st);
 }
 
 template <typename T, typename S> efla_status_t launch_scan_fwd(const scan::Args &a, long long blocks, cudaStream_t st) {
@@ -282,15 +300,14 @@ template <typename T, typename S> efla_status_t launch_scan_fwd(const scan::Args
 }
 
 template <typename T, typename S, bool VEC> efla_status_t run_scan_bwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
-    constexpr size_t smem = sizeof(scan::BwdSmem<T, S>);
+    constexpr size_t smem = sizeof(scan::BwdSmem<S>);
     if (!ensure_smem<scan::scan_bwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
     if (a.nseg > 1) {
-        scan::segment_kernel<T, S, VEC, false><<<grid, scan::kThreads, 0, st>>>(a);
-        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
-        scan::segment_kernel<T, S, VEC, true><<<grid, scan::kThreads, 0, st>>>(a);
-        if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
+        efla_status_t s = run_scan<T, S, VEC, scan::STATE>(a, grid, st);
+        if (s == EFLA_OK) s = run_scan<T, S, VEC, scan::BACK>(a, grid, st);
+        if (s != EFLA_OK) return s;
     }
-    scan::scan_bwd_kernel<T, S, VEC><<<grid, scan::kThreads, smem, st>>>(a);
+    scan::scan_bwd_kernel<T, S, VEC><<<grid, 2 * scan::kThreads, smem, st>>>(a);
     return launched();
 }
 
@@ -561,8 +578,8 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
     a.B = B; a.L = L; a.C = C; a.G = G; a.N = N; a.tpg = p.tpg; a.nseg = p.nseg; a.seg = p.seg;
     float *ws = static_cast<float *>(workspace);
     carve_segments(a, ws, false);
-    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_fwd, float, N, p.ns, a, p.blocks, st);
-    EFLA_SCAN_N(launch_scan_fwd, __nv_bfloat16, N, p.ns, a, p.blocks, st);
+    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_fwd, float, N, p, a, p.blocks, st);
+    EFLA_SCAN_N(launch_scan_fwd, __nv_bfloat16, N, p, a, p.blocks, st);
 }
 
 size_t efla_scan_bwd_workspace_size(int B, int L, int C, int G, int N) {
@@ -625,8 +642,8 @@ efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const 
     ws += z4.bc;
     carve_segments(a, ws, true);
     a.part = ws;
-    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_bwd, float, N, p.ns, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
-    EFLA_SCAN_N(launch_scan_bwd, __nv_bfloat16, N, p.ns, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
+    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_bwd, float, N, p, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
+    EFLA_SCAN_N(launch_scan_bwd, __nv_bfloat16, N, p, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
 }
 
 efla_status_t efla_scan_step(const void *x, long long ldx, const void *dt, long long lddt, const float *A,

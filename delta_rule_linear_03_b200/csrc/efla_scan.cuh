@@ -14,15 +14,22 @@
 // matrices, because every (token, channel, index) has a decay of its own.
 // That exponential bounds the forward pass: 16 a clock and SM.
 //
-// A block of 128 threads takes CT channels of one sequence; LN lanes share a
-// channel, NS state values each, in registers.  The sequence goes by in
-// tiles of TC tokens.  While a tile is worked on, the next one's rows are on
-// their way into registers.  Each (token, channel) is prepared once, by the
-// thread that loaded it (softplus, D x, gates), and passed to the lanes of
-// its channel through shared memory, as are B and C in fp32.  Sums over the
-// state index are taken for TB tokens at once: at each halving step a lane
-// sends the half of its values that its partner keeps, so TB sums over TB
-// lanes cost TB - 1 shuffles.
+// A block takes CT channels of one sequence, which goes by in tiles of TC
+// tokens.  Four of its warps run the recurrence: LN lanes share a channel, a
+// lane has NS state values of each of CP channels in registers.  Four others
+// prepare the next tile and finish the one before: softplus, gates and
+// conversions of each (token, channel) are done once, by the thread that
+// loads it, and passed on through shared memory, as are B and C in fp32.
+//
+// Shared memory is the second bound: what a lane reads a token goes through
+// 128 bytes a clock and SM, broadcast or not.  A lane with one channel and four
+// state values reads 10 bytes a value (D and D x, B, C), and its four warps
+// take longer to read than to exponentiate; with two channels they share B
+// and C, 6 bytes a value.
+//
+// Sums over the state index are taken for TB tokens at once: at each halving
+// step a lane sends the half of its values that its partner keeps, so TB sums
+// over TB lanes cost TB - 1 shuffles.
 //
 // Few channels leave SMs idle, so the sequence can be cut into segments that
 // run side by side: one pass finds each segment's final state from zero and
@@ -56,32 +63,32 @@ struct Args {
     const void *dy;
     const float *dh_L;
     float *seg_p;       // [nseg][B][C][N]: adjoints that leave a segment at its start, from zero
-    float *ckpt;        // per block: states at every kSub-th token
+    float *ckpt;        // per block: states before every SUB-th token
     float *part_bc;     // [G tpg tiles: tile within group][B][L][G][2][N]
     float *part;        // [B * nseg][C][N + 2]: dA, dD, ddt_bias
     void *dx, *ddt, *dz;
     float *dh0;
 };
 
-template <int N_, int NS_> struct Shape {
-    static constexpr int N = N_, NS = NS_;
-    static constexpr int NP = NS / 2;                  // register pairs of a lane's state
+template <int N_, int NS_, int CP_> struct Shape {
+    static constexpr int N = N_, NS = NS_, CP = CP_;
+    static constexpr int NP = NS / 2;                  // register pairs of a channel's state in a lane
     static constexpr int LN = N / NS;                  // lanes of a channel
-    static constexpr int LC = 32 / LN;                 // channels of a warp
-    static constexpr int CT = kThreads / LN;           // channels of a block
-    static constexpr int TC = CT > 32 ? 16 : 32;       // tokens of a tile
+    static constexpr int LC = 32 / LN;                 // channel groups (of CP) of a warp
+    static constexpr int CT = kThreads / LN * CP;      // channels of a block
+    static constexpr int TC = CT > 32 || CP == 2 || N == 64 ? 16 : 32;  // tokens of a tile
     static constexpr int EPT = TC * CT / kThreads;     // neighbouring channels of one token that a thread prepares
     static constexpr int VPR = CT / EPT;               // threads a token's row takes
     static constexpr int BPT = TC * N / kThreads;      // values of B (and of C) that a thread loads
     static constexpr int TB = LN < 8 ? LN : 8;         // tokens whose sums are taken together
-    static constexpr int PAD = CT % 32 == 0 ? 8 : CT / 4;  // sums of TB tokens go to different banks
-    static constexpr int CS = CT + PAD;
+    static constexpr int CS = CT + (CT % 32 == 0 ? 8 : CT / 4);  // a row of sums: those of TB tokens in different banks
 
-    // Column of channel c of token t in the rows of 16-byte entries that pass
-    // D and D x on: a thread writes EPT neighbours one after the other, so
-    // neighbouring threads' entries are put into different banks.
-    __device__ static __forceinline__ int column(int c, int t) {
-        return c ^ (c >> 3 & 7) ^ ((t & 1) * (EPT / 2));
+    // Place of channel c of token t in the rows of (D, D x): a thread writes
+    // EPT neighbours, two at a time, so neighbouring threads' pairs are put
+    // into different banks.
+    __device__ static __forceinline__ int place(int c, int t) {
+        const int p = c >> 1;
+        return ((p ^ (p >> 3 & 7) ^ ((t & 1) * (EPT / 4))) << 1) | (c & 1);
     }
 };
 
@@ -125,8 +132,12 @@ __device__ __forceinline__ f32x2 softplus_2(f32x2 v2) {
 }
 __device__ __forceinline__ float softplus_f32(float v) { return unpack2(softplus_2(twice(v))).x; }
 template <int N> __device__ __forceinline__ void softplus_all(float (&v)[N]) {
+    if constexpr (N == 1) {
+        v[0] = softplus_f32(v[0]);
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
+    for (int i = 0; i + 1 < N; i += 2) {
         const float2 t = unpack2(softplus_2(pack2(v[i], v[i + 1])));
         v[i] = t.x;
         v[i + 1] = t.y;
@@ -258,86 +269,217 @@ __device__ __forceinline__ void start_state(const Args &a, const Where &w, int c
         f32x2 own[S::NP];
         gather<S>(a.seg_h + (s * stride + bc) * S::N + n0, x, own);
 #pragma unroll
-        for (int j = 0; j < S::NP; ++j) h[j] = fma2(ex2_2(mul2(pack2(d, d), A2[j])), h[j], own[j]);
+        for (int j = 0; j < S::NP; ++j) h[j] = fma2(ex2_2(mul2(twice(d), A2[j])), h[j], own[j]);
     }
 }
 
-// A thread's part in a tile: the token and channels it prepares, the token
-// and indices of B and C it loads.
-template <typename T, typename S> struct Part {
+// A preparing thread's part in a tile: the token and channels it prepares,
+// the token and indices of B and C it loads.
+template <typename S> struct Part {
     int pt, pc, bt, bn;
     __device__ __forceinline__ Part(int tid)
         : pt(tid / S::VPR), pc(tid % S::VPR * S::EPT), bt(tid * S::BPT / S::N), bn(tid * S::BPT % S::N) {}
 };
 
-// D and D x of a token's channels, each twice, as the lanes' paired operations take them.
+// D and D x (or g) of a token's channels.
 template <typename S>
-__device__ __forceinline__ void put_steps(float4 (*sd)[S::CT], int pt, int pc, const float (&d)[S::EPT],
+__device__ __forceinline__ void put_steps(float2 (*sd)[S::CT], int pt, int pc, const float (&d)[S::EPT],
                                           const float (&u)[S::EPT]) {
+    if constexpr (S::EPT == 1) {
+        sd[pt][S::place(pc, pt)] = make_float2(d[0], u[0]);
+    } else {
 #pragma unroll
-    for (int e = 0; e < S::EPT; ++e) sd[pt][S::column(pc + e, pt)] = make_float4(d[e], d[e], u[e], u[e]);
+        for (int e = 0; e + 1 < S::EPT; e += 2)
+            *reinterpret_cast<float4 *>(&sd[pt][S::place(pc + e, pt)]) = make_float4(d[e], u[e], d[e + 1], u[e + 1]);
+    }
 }
-
-// ---------------------------------------------------------------- one segment's own maps
-// REV = false: the final state from zero (the first segment: from h0) and the
-// sum of D.  REV = true: the adjoint that leaves the segment at its start
-// when none enters at its end (u_t = C_t g_t, p <- exp(D_t A) (p + u_t)).
-template <typename T, typename S, bool VEC, bool REV>
-__global__ void __launch_bounds__(kThreads) segment_kernel(Args a) {
-    __shared__ float4 sd[S::TC][S::CT];  // D, D, and D x (or g) twice
-    __shared__ __align__(16) float sb[S::TC][S::N];
-    constexpr int NP = S::NP;
-    const Where w(a, S::CT);
-    const Part<T, S> part(threadIdx.x);
-    const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
-    const int c = w.c0 + cl, n0 = ln * S::NS, pt = part.pt, pc = part.pc;
-    const bool on = cl < w.nc;
-    f32x2 A2[NP], h[NP];
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
-    const long long bc = (long long)w.b * a.C + c;
-    if (on) {
-        gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
-        if (!REV && w.seg == 0 && a.h0) {
-            gather<S>(a.h0 + bc * S::N + n0, 0, h);
-            scatter<S>(a.seg_0 + bc * S::N + n0, 0, h);
+// The same of a lane's channels, as its paired operations take them.
+template <typename S> struct Steps {
+    f32x2 d[S::CP], u[S::CP];
+    __device__ __forceinline__ void get(const float2 *p) {
+        if constexpr (S::CP == 2) {
+            const float4 t = *reinterpret_cast<const float4 *>(p);
+            d[0] = twice(t.x);
+            u[0] = twice(t.y);
+            d[1] = twice(t.z);
+            u[1] = twice(t.w);
+        } else {
+            const float2 t = *p;
+            d[0] = twice(t.x);
+            u[0] = twice(t.y);
         }
     }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], pack2(kLog2e, kLog2e));
-    const int end = min(w.t1, w.len);
-    const int tiles = end > w.t0 ? (end - w.t0 + S::TC - 1) / S::TC : 0;
-    float bias[S::EPT];
-#pragma unroll
-    for (int i = 0; i < S::EPT; ++i) bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
+};
 
-    const long long ldx = REV ? a.C : a.ldx, ldb = REV ? a.ldc : a.ldb, ldz = a.z ? a.ldz : ldx;
-    const T *px = static_cast<const T *>(REV ? a.dy : a.x) + w.c0;
-    const T *pd = static_cast<const T *>(a.dt) + w.c0;
-    const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
-    const T *pb = static_cast<const T *>(REV ? a.Cm : a.Bm) + w.g * S::N + part.bn;
-    Raw<T, S::EPT> rx, rd, rz;
-    Raw<T, S::BPT> rb;
-    const auto load = [&](int k) {
-        const int t = w.t0 + k * S::TC;
-        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1);
-        rx = load_row<T, S::EPT, VEC>(px + row * ldx, pc, w.nc);
-        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-        if (REV) rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-        rb = load_bc<T, S::BPT, VEC>(pb + ((long long)w.b * a.L + min(t + part.bt, a.L - 1)) * ldb);
-    };
-    if (tiles) load(REV ? tiles - 1 : 0);
-    const float4 *d0 = &sd[0][S::column(cl, 0)], *d1 = &sd[0][S::column(cl, 1)];
-    for (int i = 0; i < tiles; ++i) {
-        const int k = REV ? tiles - 1 - i : i, t0 = w.t0 + k * S::TC;
-        {
-            const bool in = t0 + pt < end, inb = t0 + part.bt < end;
-            float x[S::EPT], d[S::EPT], b[S::BPT];
+__device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Where a lane of the recurrence works: first state index, channels.
+template <typename S> struct Lane {
+    int lane, ln, n0, cl;
+    bool on[S::CP];
+    __device__ __forceinline__ Lane(int tid, const Where &w)
+        : lane(tid & 31), ln(lane % S::LN), n0(ln * S::NS), cl(((tid >> 5) * S::LC + lane / S::LN) * S::CP) {
+#pragma unroll
+        for (int i = 0; i < S::CP; ++i) on[i] = cl + i < w.nc;
+    }
+};
+
+// ---------------------------------------------------------------- forward
+// FULL: outputs, from the composed state.  STATE: a segment's final state
+// from zero (the first segment's from h0) and its sum of D.  BACK: the
+// adjoint that leaves a segment at its start when none enters at its end
+// (p <- exp(D_t A) (p + C_t g_t), from the last token to the first).
+enum Mode { FULL, STATE, BACK };
+
+template <typename S> struct FwdSmem {
+    alignas(16) float2 sd[2][S::TC][S::CT];  // D, D x (or g)
+    alignas(16) float sy[2][S::TC][S::CS];   // <C, h>
+    alignas(16) float sb[2][S::TC][S::N], sc[2][S::TC][S::N];
+};
+
+template <typename T, typename S, bool VEC, Mode MODE>
+__global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(raw_smem);
+    constexpr int NP = S::NP, TC = S::TC, TB = S::TB, CP = S::CP;
+    const Where w(a, S::CT);
+    const int end = min(w.t1, w.len);
+    const int tiles = end > w.t0 ? (end - w.t0 + TC - 1) / TC : 0;               // those with tokens that count
+    const int all = MODE == FULL ? (w.t1 - w.t0 + TC - 1) / TC : tiles;          // those with outputs
+    const auto tile_of = [&](int k) { return MODE == BACK ? tiles - 1 - k : k; };  // the k-th that is worked on
+    if (threadIdx.x < kThreads) {  // the recurrence
+        const Lane<S> me(threadIdx.x, w);
+        f32x2 A2[CP][NP], h[CP][NP];
+        float sum[CP];
+#pragma unroll
+        for (int i = 0; i < CP; ++i) {
+            sum[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) A2[i][j] = h[i][j] = 0ull;
+            const int c = w.c0 + me.cl + i;
+            const long long at = ((long long)w.b * a.C + c) * S::N + me.n0;
+            if (me.on[i]) gather<S>(a.A + (long long)c * S::N + me.n0, 0, A2[i]);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) A2[i][j] = mul2(A2[i][j], twice(kLog2e));
+            if (MODE == FULL && me.on[i]) start_state<S>(a, w, c, me.n0, 0, A2[i], h[i]);
+            if (MODE == STATE && me.on[i] && w.seg == 0 && a.h0) {
+                gather<S>(a.h0 + at, 0, h[i]);
+                scatter<S>(a.seg_0 + at, 0, h[i]);
+            }
+        }
+        const int k0 = S::place(me.cl, 0), k1 = S::place(me.cl, 1), o = halved_index<TB, 1, S::LN>(me.lane) * S::CS + me.cl;
+        tile_barrier();
+        for (int k = 0; k < all; ++k) {
+            const int f = k & 1;
+            const float2 *d0 = &sm.sd[f][0][k0], *d1 = &sm.sd[f][0][k1];
+            const float *sb = &sm.sb[f][0][me.n0], *sc = &sm.sc[f][0][me.n0];
+            float *out = &sm.sy[f][0][0] + o;
+            if (k < tiles) {
+                // Decays and terms of the next PB tokens are fetched and computed beside the chain of
+                // these, and a batch's sums over the lanes wait until the next one's work is there to
+                // hide them: there may be no more than one such warp a scheduler.
+                constexpr int PB = 2;
+                f32x2 e[2][PB][CP][NP], v[2][PB][CP][NP];
+                const auto terms = [&](int s, f32x2(&e)[PB][CP][NP], f32x2(&v)[PB][CP][NP]) {
+#pragma unroll
+                    for (int u = 0; u < PB; ++u) {
+                        const int t = MODE == BACK ? TC - 1 - s - u : s + u;
+                        Steps<S> d;
+                        d.get((t & 1 ? d1 : d0) + t * S::CT);
+                        f32x2 b[NP];
+                        load_pairs<NP>(sb + t * S::N, b);
+#pragma unroll
+                        for (int i = 0; i < CP; ++i) {
+                            if (MODE == STATE) sum[i] += unpack2(d.d[i]).x;
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) {
+                                e[u][i][j] = ex2_2(mul2(d.d[i], A2[i][j]));
+                                v[u][i][j] = mul2(d.u[i], b[j]);
+                            }
+                        }
+                    }
+                };
+                float p[CP][TB];
+                const auto reduce = [&](int s) {
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) halve<TB, 1, S::LN>(p[i], me.lane);
+                    if (S::LN <= TB || me.ln < TB) {
+                        if constexpr (CP == 2) *reinterpret_cast<float2 *>(out + s * S::CS) = make_float2(p[0][0], p[1][0]);
+                        else out[s * S::CS] = p[0][0];
+                    }
+                };
+                terms(0, e[0], v[0]);
+#pragma unroll
+                for (int s = 0; s < TC; s += PB) {
+                    const int g = s / PB & 1;
+                    f32x2 q[PB][NP];
+                    if (MODE == FULL)
+#pragma unroll
+                        for (int u = 0; u < PB; ++u) load_pairs<NP>(sc + (s + u) * S::N, q[u]);
+                    if (s + PB < TC) terms(s + PB, e[g ^ 1], v[g ^ 1]);
+                    if (MODE == FULL && s % TB == 0 && s > 0) reduce(s - TB);
+#pragma unroll
+                    for (int u = 0; u < PB; ++u)
+#pragma unroll
+                        for (int i = 0; i < CP; ++i) {
+                            f32x2 y = 0ull;
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) {
+                                if (MODE == BACK) h[i][j] = mul2(e[g][u][i][j], add2(h[i][j], v[g][u][i][j]));
+                                else h[i][j] = fma2(e[g][u][i][j], h[i][j], v[g][u][i][j]);
+                                if (MODE == FULL) y = j ? fma2(h[i][j], q[u][j], y) : mul2(h[i][j], q[u][j]);
+                            }
+                            if (MODE == FULL) p[i][(s + u) % TB] = sum2(y);
+                        }
+                }
+                if (MODE == FULL) reduce(TC - TB);
+            }
+            tile_barrier();
+        }
+#pragma unroll
+        for (int i = 0; i < CP; ++i) {
+            if (!me.on[i]) continue;
+            const long long bc = (long long)w.b * a.C + w.c0 + me.cl + i, at = (long long)w.seg * a.B * a.C + bc;
+            if (MODE == FULL) {
+                if (a.h_L && w.seg == a.nseg - 1) scatter<S>(a.h_L + bc * S::N + me.n0, 0, h[i]);
+            } else {
+                scatter<S>((MODE == BACK ? a.seg_p : a.seg_h) + at * S::N + me.n0, 0, h[i]);
+                if (MODE == STATE && me.ln == 0) a.seg_d[at] = sum[i];
+            }
+        }
+    } else {  // preparation and outputs
+        const Part<S> part(threadIdx.x - kThreads);
+        const int pt = part.pt, pc = part.pc;
+        float bias[S::EPT], dskip[S::EPT];
+#pragma unroll
+        for (int i = 0; i < S::EPT; ++i) {
+            bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
+            dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
+        }
+        const long long ldx = MODE == BACK ? a.C : a.ldx, ldz = a.z ? a.ldz : ldx, ldb = MODE == BACK ? a.ldc : a.ldb;
+        const T *px = static_cast<const T *>(MODE == BACK ? a.dy : a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
+        const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+        const T *pb = static_cast<const T *>(MODE == BACK ? a.Cm : a.Bm) + w.g * S::N + part.bn;
+        const T *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
+        Raw<T, S::EPT> rx, rd, rz, mx, mz, ox, oz;  // of the tile that comes in, the one worked on, the one to finish
+        Raw<T, S::BPT> rb, rc;
+        const auto load = [&](int k) {
+            const int t = w.t0 + max(tile_of(k), 0) * TC;
+            const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
+            rx = load_row<T, S::EPT, VEC>(px + row * ldx, pc, w.nc);
+            rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+            if (MODE != STATE) rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+            rb = load_bc<T, S::BPT, VEC>(pb + rowb * ldb);
+            if (MODE == FULL) rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+        };
+        const auto prepare = [&](int k) {
+            const int t = w.t0 + tile_of(k) * TC, f = k & 1;
+            const bool in = t + pt < end, inb = t + part.bt < end;
+            float x[S::EPT], d[S::EPT], b[S::BPT], q[S::BPT];
             widen<T, S::EPT>(rx, x);
             widen<T, S::EPT>(rd, d);
             widen<T, S::BPT>(rb, b);
-            if constexpr (REV) {
+            if constexpr (MODE == BACK) {
                 float z[S::EPT];
                 widen<T, S::EPT>(rz, z);
                 if (a.z)
@@ -350,167 +492,18 @@ __global__ void __launch_bounds__(kThreads) segment_kernel(Args a) {
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
                 d[e] = in ? d[e] : 0.f;
-                x[e] = in ? (REV ? x[e] : d[e] * x[e]) : 0.f;
-            }
-            put_steps<S>(sd, pt, pc, d, x);
-#pragma unroll
-            for (int e = 0; e < S::BPT; ++e) b[e] = inb ? b[e] : 0.f;
-            store_raw<float, S::BPT>(&sb[part.bt][part.bn], narrow<float, S::BPT>(b));
-        }
-        __syncthreads();
-        if (i + 1 < tiles) load(REV ? k - 1 : k + 1);
-#pragma unroll 8
-        for (int s = 0; s < S::TC; ++s) {
-            const int t = REV ? S::TC - 1 - s : s;
-            const float4 d = (t & 1 ? d1 : d0)[t * S::CT];
-            f32x2 b[NP];
-            load_pairs<NP>(&sb[t][n0], b);
-            if (!REV) sum += d.x;
-            const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const f32x2 e = ex2_2(mul2(dd, A2[j]));
-                h[j] = REV ? mul2(e, fma2(uu, b[j], h[j])) : fma2(e, h[j], mul2(uu, b[j]));
-            }
-        }
-        __syncthreads();
-    }
-    if (!on) return;
-    const long long at = (long long)w.seg * a.B * a.C + bc;
-    scatter<S>((REV ? a.seg_p : a.seg_h) + at * S::N + n0, 0, h);
-    if (!REV && ln == 0) a.seg_d[at] = sum;
-}
-
-// ---------------------------------------------------------------- forward
-// Four warps run the recurrence, four others prepare the next tile for them
-// and finish the one before: the preparation is two thirds as many
-// instructions as the recurrence, and beside it they cost no time of their
-// own.  Two buffers, one barrier a tile.
-template <typename S> struct FwdSmem {
-    float4 sd[2][S::TC][S::CT];               // D, D, D x, D x
-    alignas(16) float sy[2][S::TC][S::CS];    // <C, h>
-    alignas(16) float sb[2][S::TC][S::N], sc[2][S::TC][S::N];
-};
-
-__device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
-    extern __shared__ __align__(16) unsigned char raw_smem[];
-    FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(raw_smem);
-    constexpr int NP = S::NP, TC = S::TC, TB = S::TB;
-    const Where w(a, S::CT);
-    const int end = min(w.t1, w.len);
-    const int all = (w.t1 - w.t0 + TC - 1) / TC;                           // tiles
-    const int tiles = end > w.t0 ? (end - w.t0 + TC - 1) / TC : 0;         // those with tokens that count
-    if (threadIdx.x < kThreads) {  // the recurrence
-        const int tid = threadIdx.x, lane = tid & 31, ln = lane % S::LN, cl = (tid >> 5) * S::LC + lane / S::LN;
-        const int c = w.c0 + cl, n0 = ln * S::NS;
-        const bool on = cl < w.nc;
-        f32x2 A2[NP], h[NP];
-#pragma unroll
-        for (int j = 0; j < NP; ++j) A2[j] = h[j] = 0ull;
-        if (on) gather<S>(a.A + (long long)c * S::N + n0, 0, A2);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) A2[j] = mul2(A2[j], twice(kLog2e));
-        if (on) start_state<S>(a, w, c, n0, 0, A2, h);
-        const int k0 = S::column(cl, 0), k1 = S::column(cl, 1), o = halved_index<TB, 1, S::LN>(lane) * S::CS + cl;
-        tile_barrier();
-        for (int k = 0; k < all; ++k) {
-            const int f = k & 1;
-            const float4 *d0 = &sm.sd[f][0][k0], *d1 = &sm.sd[f][0][k1];
-            const float *sb = &sm.sb[f][0][n0], *sc = &sm.sc[f][0][n0];
-            float *out = &sm.sy[f][0][0] + o;
-            if (k < tiles) {
-                // decays and terms of the next TB tokens are fetched and computed beside the chain of these
-                f32x2 e[2][TB][NP], v[2][TB][NP];
-                const auto terms = [&](int s, f32x2(&e)[TB][NP], f32x2(&v)[TB][NP]) {
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        const float4 d = (u & 1 ? d1 : d0)[(s + u) * S::CT];
-                        const f32x2 dd = pack2(d.x, d.y), uu = pack2(d.z, d.w);
-                        load_pairs<NP>(sb + (s + u) * S::N, v[u]);
-#pragma unroll
-                        for (int j = 0; j < NP; ++j) {
-                            e[u][j] = ex2_2(mul2(dd, A2[j]));
-                            v[u][j] = mul2(uu, v[u][j]);
-                        }
-                    }
-                };
-                terms(0, e[0], v[0]);
-#pragma unroll
-                for (int s = 0; s < TC; s += TB) {
-                    constexpr int two = 2 * TB;
-                    const int g = s % two / TB;
-                    f32x2 q[TB][NP];
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) load_pairs<NP>(sc + (s + u) * S::N, q[u]);
-                    if (s + TB < TC) terms(s + TB, e[g ^ 1], v[g ^ 1]);
-                    float p[TB];
-#pragma unroll
-                    for (int u = 0; u < TB; ++u) {
-                        f32x2 y = 0ull;
-#pragma unroll
-                        for (int j = 0; j < NP; ++j) {
-                            h[j] = fma2(e[g][u][j], h[j], v[g][u][j]);
-                            y = j ? fma2(h[j], q[u][j], y) : mul2(h[j], q[u][j]);
-                        }
-                        p[u] = sum2(y);
-                    }
-                    halve<TB, 1, S::LN>(p, lane);
-                    if (S::LN <= TB || ln < TB) out[s * S::CS] = p[0];
-                }
-            }
-            tile_barrier();
-        }
-        if (a.h_L && on && w.seg == a.nseg - 1) scatter<S>(a.h_L + ((long long)w.b * a.C + c) * S::N + n0, 0, h);
-    } else {  // preparation and outputs
-        const Part<T, S> part(threadIdx.x - kThreads);
-        const int pt = part.pt, pc = part.pc;
-        float bias[S::EPT], dskip[S::EPT];
-#pragma unroll
-        for (int i = 0; i < S::EPT; ++i) {
-            bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
-            dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
-        }
-        const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
-        const T *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
-        const long long ldz = a.z ? a.ldz : a.ldx;
-        const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
-        Raw<T, S::EPT> rx, rd, rz, mx, mz, ox, oz;  // of the tile that comes in, the one worked on, the one to finish
-        Raw<T, S::BPT> rb, rc;
-        const auto load = [&](int k) {
-            const int t = w.t0 + k * TC;
-            const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
-            rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
-            rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-            rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-            rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
-            rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
-        };
-        const auto prepare = [&](int k) {
-            const int t = w.t0 + k * TC, f = k & 1;
-            const bool in = t + pt < end, inb = t + part.bt < end;
-            float x[S::EPT], d[S::EPT], b[S::BPT], q[S::BPT];
-            widen<T, S::EPT>(rx, x);
-            widen<T, S::EPT>(rd, d);
-            widen<T, S::BPT>(rb, b);
-            widen<T, S::BPT>(rc, q);
-#pragma unroll
-            for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
-            if (a.softplus) softplus_all<S::EPT>(d);
-#pragma unroll
-            for (int e = 0; e < S::EPT; ++e) {
-                d[e] = in ? d[e] : 0.f;
-                x[e] = in ? d[e] * x[e] : 0.f;
+                x[e] = in ? (MODE == BACK ? x[e] : d[e] * x[e]) : 0.f;
             }
             put_steps<S>(sm.sd[f], pt, pc, d, x);
 #pragma unroll
-            for (int e = 0; e < S::BPT; ++e) {
-                b[e] = inb ? b[e] : 0.f;
-                q[e] = inb ? q[e] : 0.f;
-            }
+            for (int e = 0; e < S::BPT; ++e) b[e] = inb ? b[e] : 0.f;
             store_raw<float, S::BPT>(&sm.sb[f][part.bt][part.bn], narrow<float, S::BPT>(b));
-            store_raw<float, S::BPT>(&sm.sc[f][part.bt][part.bn], narrow<float, S::BPT>(q));
+            if constexpr (MODE == FULL) {
+                widen<T, S::BPT>(rc, q);
+#pragma unroll
+                for (int e = 0; e < S::BPT; ++e) q[e] = inb ? q[e] : 0.f;
+                store_raw<float, S::BPT>(&sm.sc[f][part.bt][part.bn], narrow<float, S::BPT>(q));
+            }
         };
         const auto finish = [&](int k) {
             const int t = w.t0 + k * TC, f = k & 1;
@@ -536,357 +529,443 @@ template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(2 
         load(1);
         tile_barrier();
         for (int k = 0; k < all; ++k) {
-            prepare(k + 1);  // past the last tile: zeros that nothing reads
+            if (MODE != BACK || k + 1 < all) prepare(k + 1);  // past the last tile: zeros that nothing reads
             const Raw<T, S::EPT> nx = rx, nz = rz;
             load(k + 2);
-            if (k > 0) finish(k - 1);
+            if (MODE == FULL && k > 0) finish(k - 1);
             ox = mx;
             oz = mz;
             mx = nx;
             mz = nz;
             tile_barrier();
         }
-        finish(all - 1);
+        if (MODE == FULL) finish(all - 1);
     }
 }
 
 // ---------------------------------------------------------------- backward
-// Two walks over the segment.  The first repeats the forward recurrence and
-// leaves the state before every kSub-th token in the workspace, one vector a
-// thread, where the second finds it in reverse order.  The second goes
-// backwards: for kSub tokens at a time it recomputes decays and states into
-// registers from that state, and then runs the adjoint down through them.
+// Two walks over the segment, each with four warps that run the recurrence
+// and four that prepare and finish, as in the forward pass.  The first walk
+// repeats the forward recurrence and leaves the state before every SUB-th
+// token in the workspace, one vector a thread, where the second finds it in
+// reverse order.  The second goes backwards: for SUB tokens at a time it
+// recomputes decays and states into registers from that state, and then runs
+// the adjoint down through them.
 //
-// dB and dC are sums over channels: a lane's 2 NS products of a token are
-// halved over the warp's channel lanes, then added over the block's warps in
-// shared memory, and reach the workspace as one partial row a block; those
-// and the sums over sequences (dA, dD, ddt_bias) are added by kernels of
-// their own in a fixed order.  So that halving needs no selection, a lane
-// whose channel bit says "keep the upper half" has its state values in the
-// registers in swapped order (register j: state n0 + (j ^ x)), and reads B
-// and C from a copy in that order.
-constexpr int kSub = 8;
+// dB and dC are sums over channels: a lane's 2 NS products of a token (its
+// channels' added) are halved over the warp's channel lanes, then added over
+// the block's warps in shared memory, and reach the workspace as one partial
+// row a block; those and the sums over sequences (dA, dD, ddt_bias) are added
+// by kernels of their own in a fixed order.  So that halving needs no
+// selection, a lane whose channel bit says "keep the upper half" has its state
+// values in the registers in swapped order (register j: state n0 + (j ^ x)),
+// and reads B and C from a copy in that order.
 
-template <typename T, typename S> struct BwdSmem {
+template <typename S> struct BwdSmem {
     static constexpr int COPY = S::TC * S::N + 16;  // one order's copy; the next begins 16 banks on
-    float4 sd[S::TC][S::CT];                        // D, D, D x, D x
-    float2 sg[S::TC][S::CT];                        // g, g
-    alignas(16) float s1[S::TC][S::CS];             // <p, B>
-    alignas(16) float s2[S::TC][S::CS];             // <p e h, A>
-    alignas(16) float s3[S::TC][S::CS];             // <C, h>
-    alignas(16) float sb[S::NS][COPY];
-    alignas(16) float sc[S::NS][COPY];
-    float bc[kThreads / 32][S::TC][2][S::N];        // a warp's sums over its channels
+    alignas(16) float2 sd[2][S::TC][S::CT];         // D, D x
+    alignas(16) float sg[2][S::TC][S::CS];          // g
+    alignas(16) float s1[2][S::TC][S::CS];          // <p, B>
+    alignas(16) float s2[2][S::TC][S::CS];          // <p e h, A>
+    alignas(16) float s3[2][S::TC][S::CS];          // <C, h>
+    alignas(16) float sb[2][S::NS + 1][COPY];       // the last: zeros, for lanes without a channel
+    alignas(16) float sc[2][S::NS + 1][COPY];
+    alignas(16) float bc[2][kThreads / 32][S::TC][2][S::N];  // a warp's sums over its channels
 };
 
-template <typename T, typename S, bool VEC> __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(Args a) {
+template <typename T, typename S, bool VEC>
+__global__ void __launch_bounds__(2 * kThreads) scan_bwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
-    BwdSmem<T, S> &sm = *reinterpret_cast<BwdSmem<T, S> *>(raw_smem);
-    constexpr int NS = S::NS, NP = S::NP, LN = S::LN, TC = S::TC, TB = S::TB;
+    BwdSmem<S> &sm = *reinterpret_cast<BwdSmem<S> *>(raw_smem);
+    constexpr int NS = S::NS, NP = S::NP, LN = S::LN, TC = S::TC, TB = S::TB, CP = S::CP, SUB = NS * CP >= 8 ? 4 : 8;
+    constexpr int QB = TB < SUB ? TB : SUB;  // tokens whose sums over the state index are taken together
     const Where w(a, S::CT);
-    const Part<T, S> part(threadIdx.x);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane % LN, cl = warp * S::LC + lane / LN;
-    const int c = w.c0 + cl, n0 = ln * NS, pt = part.pt, pc = part.pc;
-    const int ox = halved_index<NS, LN, 32>(lane);  // the order of this lane's states
-    const bool on = cl < w.nc;
-    const long long bc = (long long)w.b * a.C + c;
-    const f32x2 l2e = pack2(kLog2e, kLog2e), minus = pack2(-1.f, -1.f);
-    f32x2 A1[NP], A2[NP], h[NP], p[NP], dA[NP], lost[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A1[j] = h[j] = p[j] = dA[j] = lost[j] = 0ull;
-    if (on) gather<S>(a.A + (long long)c * S::N + n0, ox, A1);
-#pragma unroll
-    for (int j = 0; j < NP; ++j) A2[j] = mul2(A1[j], l2e);
-    if (on) start_state<S>(a, w, c, n0, ox, A2, h);
     const int end = min(w.t1, w.len);
     const int tiles = end > w.t0 ? (end - w.t0 + TC - 1) / TC : 0;
-    float bias[S::EPT], dskip[S::EPT], aD[S::EPT], ab[S::EPT];
-#pragma unroll
-    for (int i = 0; i < S::EPT; ++i) {
-        bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
-        dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
-        aD[i] = ab[i] = 0.f;
-    }
-    float *ck = a.ckpt + ((long long)blockIdx.x * (a.seg / kSub) * kThreads + tid) * NS;
-
-    const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
-    const T *py = static_cast<const T *>(a.dy) + w.c0, *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
-    const long long ldz = a.z ? a.ldz : a.ldx;
-    const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
-    Raw<T, S::EPT> rx, rd, rz, ry;
-    Raw<T, S::BPT> rb, rc;
-    const auto load = [&](int t, bool back) {
-        const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
-        rx = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
-        rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-        rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
-        if (back) {
-            ry = load_row<T, S::EPT, VEC>(py + row * a.C, pc, w.nc);
-            rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-            rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
-        }
-    };
-    // B or C of the tile, zeros past the end, in every lane's order
-    const auto put_bc = [&](float (*to)[BwdSmem<T, S>::COPY], const Raw<T, S::BPT> &r, bool inb) {
-        float v[S::BPT];
-        widen<T, S::BPT>(r, v);
-#pragma unroll
-        for (int e = 0; e < S::BPT; ++e) v[e] = inb ? v[e] : 0.f;
-        const int at = part.bt * S::N + part.bn;
-#pragma unroll
-        for (int k = 0; k < NS; ++k) {
-            if constexpr (S::BPT % 4 == 0) {
-#pragma unroll
-                for (int e = 0; e < S::BPT; e += 4)
-                    *reinterpret_cast<float4 *>(&to[k][at + e]) = make_float4(v[e ^ k], v[(e + 1) ^ k], v[(e + 2) ^ k], v[(e + 3) ^ k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < S::BPT; ++e) to[k][(at + e) ^ k] = v[e];
-            }
-        }
-    };
-    const auto put_tile = [&](bool in, float (&x)[S::EPT], float (&d)[S::EPT]) {
-#pragma unroll
-        for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
-        if (a.softplus) softplus_all<S::EPT>(d);
-#pragma unroll
-        for (int e = 0; e < S::EPT; ++e) {
-            d[e] = in ? d[e] : 0.f;
-            x[e] = in ? d[e] * x[e] : 0.f;
-        }
-        put_steps<S>(sm.sd, pt, pc, d, x);
-    };
-    const float4 *d0 = &sm.sd[0][S::column(cl, 0)], *d1 = &sm.sd[0][S::column(cl, 1)];
-    const float2 *g0 = &sm.sg[0][S::column(cl, 0)], *g1 = &sm.sg[0][S::column(cl, 1)];
-    const float *lb = &sm.sb[ox][n0], *lc = &sm.sc[ox][n0];
-
-    if (tiles) load(w.t0, false);
-    for (int i = 0; i < tiles; ++i) {
-        const int t = w.t0 + i * TC;
-        float x[S::EPT], d[S::EPT];
-        widen<T, S::EPT>(rx, x);
-        widen<T, S::EPT>(rd, d);
-        put_tile(t + pt < end, x, d);
-        put_bc(sm.sb, rb, t + part.bt < end);
-        __syncthreads();
-        if (i + 1 < tiles) load(t + TC, false);
-#pragma unroll 1
-        for (int s = 0; s < TC; s += kSub) {
-            store_pairs<NP>(ck + (long long)((i * TC + s) / kSub) * kThreads * NS, h);
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
-                const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w);
-                f32x2 b[NP];
-                load_pairs<NP>(lb + (s + u) * S::N, b);
-#pragma unroll
-                for (int j = 0; j < NP; ++j) h[j] = fma2(ex2_2(mul2(dd, A2[j])), h[j], mul2(uu, b[j]));
-            }
-        }
-        __syncthreads();
-    }
-
-    // the adjoint that enters at the segment's end
-    if (on) {
-        if (a.dh_L) gather<S>(a.dh_L + bc * S::N + n0, ox, p);
-        const long long stride = (long long)a.B * a.C;
-        for (int s = a.nseg - 1; s > w.seg; --s) {
-            const float d = a.seg_d[s * stride + bc];
-            f32x2 own[NP];
-            gather<S>(a.seg_p + (s * stride + bc) * S::N + n0, ox, own);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) p[j] = fma2(ex2_2(mul2(pack2(d, d), A2[j])), p[j], own[j]);
-        }
-    }
     const int all = (w.t1 - w.t0 + TC - 1) / TC;  // tiles with padding: their outputs are zeros
-    if (tiles) load(w.t0 + (tiles - 1) * TC, true);
-    for (int i = all - 1; i >= 0; --i) {
-        const int t = w.t0 + i * TC;
-        const bool in = t + pt < end;
-        const Raw<T, S::EPT> cx = rx, cd = rd, cz = rz, cy = ry;
-        float d[S::EPT], g[S::EPT];
+    float *sums = a.part + (long long)(w.seg * a.B + w.b) * a.C * (S::N + 2);
+    if (threadIdx.x < kThreads) {  // the recurrences
+        const int tid = threadIdx.x, warp = tid >> 5;
+        const Lane<S> me(tid, w);
+        const int lane = me.lane, n0 = me.n0, ox = halved_index<NS, LN, 32>(lane);  // the order of this lane's states
+        const int copy = me.on[0] ? ox : NS;
+        f32x2 A2[CP][NP], h[CP][NP];
 #pragma unroll
-        for (int e = 0; e < S::EPT; ++e) d[e] = g[e] = 0.f;
-        if (i < tiles) {
-            float x[S::EPT], z[S::EPT];
-            widen<T, S::EPT>(rx, x);
-            widen<T, S::EPT>(rd, d);
-            widen<T, S::EPT>(ry, g);
-            widen<T, S::EPT>(rz, z);
-            put_tile(in, x, d);
+        for (int i = 0; i < CP; ++i) {
 #pragma unroll
-            for (int e = 0; e < S::EPT; ++e) {
-                if (a.z) g[e] *= silu_f32(z[e]);
-                g[e] = in ? g[e] : 0.f;
-                sm.sg[pt][S::column(pc + e, pt)] = make_float2(g[e], g[e]);
-            }
-            put_bc(sm.sb, rb, t + part.bt < end);
-            put_bc(sm.sc, rc, t + part.bt < end);
-            __syncthreads();
-            if (i > 0) load(t - TC, true);
-            f32x2 next[NP];
-            load_pairs<NP>(ck + (long long)((i * TC + TC - kSub) / kSub) * kThreads * NS, next);
-#pragma unroll 1
-            for (int s = TC - kSub; s >= 0; s -= kSub) {
-                f32x2 hs[kSub + 1][NP], es[kSub][NP], part_dA[NP];
+            for (int j = 0; j < NP; ++j) A2[i][j] = h[i][j] = 0ull;
+            if (me.on[i]) gather<S>(a.A + (long long)(w.c0 + me.cl + i) * S::N + n0, ox, A2[i]);
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    hs[0][j] = next[j];
-                    part_dA[j] = 0ull;
-                }
-                if (s > 0) load_pairs<NP>(ck + (long long)((i * TC + s) / kSub - 1) * kThreads * NS, next);
+            for (int j = 0; j < NP; ++j) A2[i][j] = mul2(A2[i][j], twice(kLog2e));
+            if (me.on[i]) start_state<S>(a, w, w.c0 + me.cl + i, n0, ox, A2[i], h[i]);
+        }
+        constexpr int CKS = kThreads * NS * CP;  // floats of one checkpoint of the block
+        float *ck = a.ckpt + (long long)blockIdx.x * (a.seg / SUB) * CKS + tid * NS;
+        const int k0 = S::place(me.cl, 0), k1 = S::place(me.cl, 1);
+        tile_barrier();
+        for (int k = 0; k < tiles; ++k) {
+            const int f = k & 1;
+            const float2 *d0 = &sm.sd[f][0][k0], *d1 = &sm.sd[f][0][k1];
+            const float *lb = &sm.sb[f][copy][n0];
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
-                    const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w);
+            for (int s = 0; s < TC; s += SUB) {
+#pragma unroll
+                for (int i = 0; i < CP; ++i) store_pairs<NP>(ck + (long long)((k * TC + s) / SUB) * CKS + i * kThreads * NS, h[i]);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    Steps<S> d;
+                    d.get((u & 1 ? d1 : d0) + (s + u) * S::CT);
                     f32x2 b[NP];
                     load_pairs<NP>(lb + (s + u) * S::N, b);
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        es[u][j] = ex2_2(mul2(dd, A2[j]));
-                        hs[u + 1][j] = fma2(es[u][j], hs[u][j], mul2(uu, b[j]));
-                    }
+                    for (int i = 0; i < CP; ++i)
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) h[i][j] = fma2(ex2_2(mul2(d.d[i], A2[i][j])), h[i][j], mul2(d.u[i], b[j]));
                 }
+            }
+            tile_barrier();
+        }
+
+        // the adjoint that enters at the segment's end
+        f32x2 A1[CP][NP], p[CP][NP], dA[CP][NP], lost[CP][NP], next[CP][NP];
 #pragma unroll
-                for (int u0 = kSub - TB; u0 >= 0; u0 -= TB) {
-                    float q1[TB], q2[TB], q3[TB];
+        for (int i = 0; i < CP; ++i) {
 #pragma unroll
-                    for (int uu0 = TB - 1; uu0 >= 0; --uu0) {
-                        const int u = u0 + uu0;
-                        const float4 v = (u & 1 ? d1 : d0)[(s + u) * S::CT];
-                        const float2 gv = (u & 1 ? g1 : g0)[(s + u) * S::CT];
-                        const f32x2 dd = pack2(v.x, v.y), uu = pack2(v.z, v.w), gg = pack2(gv.x, gv.y);
-                        f32x2 b[NP], q[NP], y1 = 0ull, y2 = 0ull, y3 = 0ull;
-                        load_pairs<NP>(lb + (s + u) * S::N, b);
-                        load_pairs<NP>(lc + (s + u) * S::N, q);
-                        float m[2 * NS];  // for each register j: dB, dC
+            for (int j = 0; j < NP; ++j) A1[i][j] = p[i][j] = dA[i][j] = lost[i][j] = 0ull;
+            if (!me.on[i]) continue;
+            const long long bc = (long long)w.b * a.C + w.c0 + me.cl + i, stride = (long long)a.B * a.C;
+            gather<S>(a.A + (long long)(w.c0 + me.cl + i) * S::N + n0, ox, A1[i]);
+            if (a.dh_L) gather<S>(a.dh_L + bc * S::N + n0, ox, p[i]);
+            for (int s = a.nseg - 1; s > w.seg; --s) {
+                const float d = a.seg_d[s * stride + bc];
+                f32x2 own[NP];
+                gather<S>(a.seg_p + (s * stride + bc) * S::N + n0, ox, own);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) p[i][j] = fma2(ex2_2(mul2(twice(d), A2[i][j])), p[i][j], own[j]);
+            }
+        }
+        if (tiles)
+#pragma unroll
+            for (int i = 0; i < CP; ++i)
+                load_pairs<NP>(ck + (long long)(tiles * TC / SUB - 1) * CKS + i * kThreads * NS, next[i]);
+        tile_barrier();
+        for (int i0 = all - 1; i0 >= 0; --i0) {
+            const int f = i0 & 1;
+            const float2 *d0 = &sm.sd[f][0][k0], *d1 = &sm.sd[f][0][k1];
+            const float *sg = &sm.sg[f][0][me.cl], *lb = &sm.sb[f][copy][n0], *lc = &sm.sc[f][copy][n0];
+            if (i0 < tiles) {
+#pragma unroll 1
+                for (int s = TC - SUB; s >= 0; s -= SUB) {
+                    f32x2 hs[SUB + 1][CP][NP], es[SUB][CP][NP], part_dA[CP][NP];
+#pragma unroll
+                    for (int i = 0; i < CP; ++i)
 #pragma unroll
                         for (int j = 0; j < NP; ++j) {
-                            p[j] = fma2(q[j], gg, p[j]);
-                            const float2 mb = unpack2(mul2(p[j], uu)), mc = unpack2(mul2(hs[u + 1][j], gg));
-                            m[4 * j] = on ? mb.x : 0.f;  // no channel: 0 even beside an infinite B or C
-                            m[4 * j + 1] = on ? mc.x : 0.f;
-                            m[4 * j + 2] = on ? mb.y : 0.f;
-                            m[4 * j + 3] = on ? mc.y : 0.f;
-                            y1 = j ? fma2(p[j], b[j], y1) : mul2(p[j], b[j]);
-                            y3 = j ? fma2(hs[u + 1][j], q[j], y3) : mul2(hs[u + 1][j], q[j]);
-                            p[j] = mul2(p[j], es[u][j]);
-                            const f32x2 r = mul2(p[j], hs[u][j]);
-                            y2 = j ? fma2(r, A1[j], y2) : mul2(r, A1[j]);
-                            part_dA[j] = fma2(r, dd, part_dA[j]);
+                            hs[0][i][j] = next[i][j];
+                            part_dA[i][j] = 0ull;
                         }
-                        q1[uu0] = sum2(y1);
-                        q2[uu0] = sum2(y2);
-                        q3[uu0] = sum2(y3);
-                        // over the channel lanes: first the state bits, by the lanes' orders, then dB from dC
-                        constexpr int SB = NS == 4 ? (S::LC >= 4 ? 2 : 1) : 1;  // state bits that are halved
-                        constexpr int V1 = 2 * NS >> SB, ST = LN << SB;
-                        if constexpr (SB == 2) {
+                    const int before = max((i0 * TC + s) / SUB - 1, 0);
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) load_pairs<NP>(ck + (long long)before * CKS + i * kThreads * NS, next[i]);
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        Steps<S> d;
+                        d.get((u & 1 ? d1 : d0) + (s + u) * S::CT);
+                        f32x2 b[NP];
+                        load_pairs<NP>(lb + (s + u) * S::N, b);
+#pragma unroll
+                        for (int i = 0; i < CP; ++i)
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) {
+                                es[u][i][j] = ex2_2(mul2(d.d[i], A2[i][j]));
+                                hs[u + 1][i][j] = fma2(es[u][i][j], hs[u][i][j], mul2(d.u[i], b[j]));
+                            }
+                    }
+#pragma unroll
+                    for (int u0 = SUB - QB; u0 >= 0; u0 -= QB) {
+                        float q1[CP][QB], q2[CP][QB], q3[CP][QB];
+#pragma unroll
+                        for (int r = QB - 1; r >= 0; --r) {
+                            const int u = u0 + r;
+                            Steps<S> d;
+                            d.get((u & 1 ? d1 : d0) + (s + u) * S::CT);
+                            f32x2 b[NP], q[NP], gg[CP];
+                            load_pairs<NP>(lb + (s + u) * S::N, b);
+                            load_pairs<NP>(lc + (s + u) * S::N, q);
+                            if constexpr (CP == 2) {
+                                const float2 t = *reinterpret_cast<const float2 *>(sg + (s + u) * S::CS);
+                                gg[0] = twice(t.x);
+                                gg[1] = twice(t.y);
+                            } else {
+                                gg[0] = twice(sg[(s + u) * S::CS]);
+                            }
+                            f32x2 mb[NP], mc[NP];
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) mb[j] = mc[j] = 0ull;
+#pragma unroll
+                            for (int i = 0; i < CP; ++i) {
+                                f32x2 y1 = 0ull, y2 = 0ull, y3 = 0ull;
+                                // Half a pair's channels may be none where rows are not whole vectors: those
+                                // add nothing, even beside an infinite B or C.
+                                const bool add = VEC || i == 0 || me.on[i];
+#pragma unroll
+                                for (int j = 0; j < NP; ++j) {
+                                    f32x2 &pj = p[i][j];
+                                    pj = fma2(q[j], gg[i], pj);
+                                    if (add) {
+                                        mb[j] = i ? fma2(pj, d.u[i], mb[j]) : mul2(pj, d.u[i]);
+                                        mc[j] = i ? fma2(hs[u + 1][i][j], gg[i], mc[j]) : mul2(hs[u + 1][i][j], gg[i]);
+                                    }
+                                    y1 = j ? fma2(pj, b[j], y1) : mul2(pj, b[j]);
+                                    y3 = j ? fma2(hs[u + 1][i][j], q[j], y3) : mul2(hs[u + 1][i][j], q[j]);
+                                    pj = mul2(pj, es[u][i][j]);
+                                    const f32x2 back = mul2(pj, hs[u][i][j]);
+                                    y2 = j ? fma2(back, A1[i][j], y2) : mul2(back, A1[i][j]);
+                                    part_dA[i][j] = fma2(back, d.d[i], part_dA[i][j]);
+                                }
+                                q1[i][r] = sum2(y1);
+                                q2[i][r] = sum2(y2);
+                                q3[i][r] = sum2(y3);
+                            }
+                            float m[2 * NS];  // of each register j: dB, dC
+#pragma unroll
+                            for (int j = 0; j < NP; ++j) {
+                                const float2 tb = unpack2(mb[j]), tc = unpack2(mc[j]);
+                                m[4 * j] = tb.x;
+                                m[4 * j + 1] = tc.x;
+                                m[4 * j + 2] = tb.y;
+                                m[4 * j + 3] = tc.y;
+                            }
+                            // over the channel lanes: first the state bits, by the lanes' orders, then dB from dC
+                            constexpr int SB = NS == 4 ? (S::LC >= 4 ? 2 : 1) : 1;  // state bits that are halved
+                            constexpr int V1 = 2 * NS >> SB, ST = LN << SB;
 #pragma unroll
                             for (int k = 0; k < NS; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS], LN);
+                            if constexpr (SB == 2)
 #pragma unroll
-                            for (int k = 0; k < NS / 2; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS / 2], 2 * LN);
-                        } else {
+                                for (int k = 0; k < NS / 2; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS / 2], 2 * LN);
+                            // left: V1 / 2 states (registers 0 ..), dB and dC of each
+                            if constexpr (ST < 32) {
+                                static_assert(V1 == 2, "one state is left where lanes are");
+                                halve<2, ST, 32>(m, lane);
+                                sm.bc[f][warp][s + u][(lane & ST) ? 1 : 0][n0 + ox] = m[0];
+                            } else {
 #pragma unroll
-                            for (int k = 0; k < NS; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS], LN);
+                                for (int k = 0; k < V1; ++k) sm.bc[f][warp][s + u][k & 1][n0 + ((k >> 1) ^ ox)] = m[k];
+                            }
                         }
-                        // left: V1 / 2 states (registers 0 ..), dB and dC of each
-                        if constexpr (ST < 32) {
-                            static_assert(V1 == 2, "one state is left where lanes are");
-                            halve<2, ST, 32>(m, lane);
-                            sm.bc[warp][s + u][(lane & ST) ? 1 : 0][n0 + ox] = m[0];
-                        } else {
+                        const int tt = s + u0 + halved_index<QB, 1, LN>(lane);
 #pragma unroll
-                            for (int k = 0; k < V1; ++k) sm.bc[warp][s + u][k & 1][n0 + ((k >> 1) ^ ox)] = m[k];
+                        for (int i = 0; i < CP; ++i) {
+                            halve<QB, 1, LN>(q1[i], lane);
+                            halve<QB, 1, LN>(q2[i], lane);
+                            if (a.z) halve<QB, 1, LN>(q3[i], lane);
+                            if (LN <= QB || me.ln < QB) {
+                                sm.s1[f][tt][me.cl + i] = q1[i][0];
+                                sm.s2[f][tt][me.cl + i] = q2[i][0];
+                                sm.s3[f][tt][me.cl + i] = q3[i][0];
+                            }
                         }
                     }
-                    halve<TB, 1, LN>(q1, lane);
-                    halve<TB, 1, LN>(q2, lane);
-                    if (a.z) halve<TB, 1, LN>(q3, lane);
-                    if (LN <= TB || ln < TB) {
-                        const int tt = s + u0 + halved_index<TB, 1, LN>(lane);
-                        sm.s1[tt][cl] = q1[0];
-                        sm.s2[tt][cl] = q2[0];
-                        sm.s3[tt][cl] = q3[0];
-                    }
-                }
-                // the long sum over tokens, with what its additions lose carried on
+                    // the long sum over tokens, with what its additions lose carried on
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const f32x2 add = add2(part_dA[j], lost[j]), to = add2(dA[j], add);
-                    lost[j] = add2(add, fma2(to, minus, dA[j]));
-                    dA[j] = to;
+                    for (int i = 0; i < CP; ++i)
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) {
+                            const f32x2 add = add2(part_dA[i][j], lost[i][j]), to = add2(dA[i][j], add);
+                            lost[i][j] = add2(add, fma2(to, twice(-1.f), dA[i][j]));
+                            dA[i][j] = to;
+                        }
                 }
             }
-            __syncthreads();
+            tile_barrier();
         }
-        if (t + pt < w.t1 && pc < w.nc) {
-            float x[S::EPT], v[S::EPT], y[S::EPT], z[S::EPT], q1[S::EPT], q2[S::EPT], q3[S::EPT];
-            widen<T, S::EPT>(cx, x);
-            widen<T, S::EPT>(cd, v);
-            widen<T, S::EPT>(cy, y);
-            widen<T, S::EPT>(cz, z);
-            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s1[pt][pc]), q1);
-            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s2[pt][pc]), q2);
-            widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s3[pt][pc]), q3);
+#pragma unroll
+        for (int i = 0; i < CP; ++i)
+            if (me.on[i]) {
+                const int c = w.c0 + me.cl + i;
+                if (w.seg == 0 && a.dh0) scatter<S>(a.dh0 + ((long long)w.b * a.C + c) * S::N + n0, ox, p[i]);
+                scatter<S>(sums + (long long)c * S::N + n0, ox, dA[i]);
+            }
+    } else {  // preparation and outputs
+        const int tid = threadIdx.x - kThreads;
+        const Part<S> part(tid);
+        const int pt = part.pt, pc = part.pc;
+        float bias[S::EPT], dskip[S::EPT], aD[S::EPT], ab[S::EPT];
+#pragma unroll
+        for (int i = 0; i < S::EPT; ++i) {
+            bias[i] = a.dt_bias && pc + i < w.nc ? a.dt_bias[w.c0 + pc + i] : 0.f;
+            dskip[i] = a.D && pc + i < w.nc ? a.D[w.c0 + pc + i] : 0.f;
+            aD[i] = ab[i] = 0.f;
+        }
+        const T *px = static_cast<const T *>(a.x) + w.c0, *pd = static_cast<const T *>(a.dt) + w.c0;
+        const T *py = static_cast<const T *>(a.dy) + w.c0, *pz = a.z ? static_cast<const T *>(a.z) + w.c0 : px;
+        const long long ldz = a.z ? a.ldz : a.ldx;
+        const T *pb = static_cast<const T *>(a.Bm) + w.g * S::N + part.bn, *pq = static_cast<const T *>(a.Cm) + w.g * S::N + part.bn;
+        // lanes without a channel meet zeros alone, so that they add zeros to dB and dC
+        for (int k = tid; k < 2 * BwdSmem<S>::COPY; k += kThreads) {
+            sm.sb[k & 1][NS][k >> 1] = 0.f;
+            sm.sc[k & 1][NS][k >> 1] = 0.f;
+        }
+        struct Rows {
+            Raw<T, S::EPT> x, d, y, z;
+        };
+        Rows in_, mid, old;  // of the tile that comes in, the one worked on, the one to finish
+        Raw<T, S::BPT> rb, rc;
+        const auto load = [&](int i, bool back) {
+            const int t = w.t0 + max(i, 0) * TC;
+            const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
+            in_.x = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
+            in_.d = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
+            rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
+            if (back) {
+                in_.y = load_row<T, S::EPT, VEC>(py + row * a.C, pc, w.nc);
+                in_.z = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
+                rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+            }
+        };
+        // B or C of the tile, zeros past the end, in every lane's order
+        const auto put_bc = [&](float (*to)[BwdSmem<S>::COPY], const Raw<T, S::BPT> &r, bool inb) {
+            float v[S::BPT];
+            widen<T, S::BPT>(r, v);
+#pragma unroll
+            for (int e = 0; e < S::BPT; ++e) v[e] = inb ? v[e] : 0.f;
+            const int at = part.bt * S::N + part.bn;
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                if constexpr (S::BPT % 4 == 0) {
+#pragma unroll
+                    for (int e = 0; e < S::BPT; e += 4)
+                        *reinterpret_cast<float4 *>(&to[k][at + e]) = make_float4(v[e ^ k], v[(e + 1) ^ k], v[(e + 2) ^ k], v[(e + 3) ^ k]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < S::BPT; ++e) to[k][(at + e) ^ k] = v[e];
+                }
+            }
+        };
+        const auto prepare = [&](int i, bool back) {
+            const int t = w.t0 + i * TC, f = i & 1;
+            const bool inb = t + part.bt < end;
+            bool in[S::EPT];
+#pragma unroll
+            for (int e = 0; e < S::EPT; ++e) in[e] = t + pt < end && pc + (VEC ? 0 : e) < w.nc;
+            float x[S::EPT], d[S::EPT];
+            widen<T, S::EPT>(in_.x, x);
+            widen<T, S::EPT>(in_.d, d);
+#pragma unroll
+            for (int e = 0; e < S::EPT; ++e) d[e] += bias[e];
+            if (a.softplus) softplus_all<S::EPT>(d);
 #pragma unroll
             for (int e = 0; e < S::EPT; ++e) {
-                q2[e] = fmaf(x[e], q1[e], q2[e]);
-                if (a.softplus) q2[e] *= sigmoid_f32(v[e] + bias[e]);
-                q1[e] = fmaf(d[e], q1[e], dskip[e] * g[e]);
-                if (a.z) z[e] = y[e] * fmaf(dskip[e], x[e], q3[e]) * dsilu_f32(z[e]);
-                q1[e] = in ? q1[e] : 0.f;
-                q2[e] = in ? q2[e] : 0.f;
-                z[e] = in ? z[e] : 0.f;
-                ab[e] += q2[e];
-                aD[e] += in ? g[e] * x[e] : 0.f;
+                d[e] = in[e] ? d[e] : 0.f;
+                x[e] = in[e] ? d[e] * x[e] : 0.f;
             }
-            const long long at = ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
-            const auto put = [&](void *to, const float (&o)[S::EPT]) {
-                const Raw<T, S::EPT> r = narrow<T, S::EPT>(o);
-                if constexpr (VEC) store_raw<T, S::EPT>(static_cast<T *>(to) + at, r);
-                else store_raw_any<T, S::EPT>(static_cast<T *>(to) + at, r, w.nc - pc);
-            };
-            put(a.dx, q1);
-            put(a.ddt, q2);
-            if (a.z) put(a.dz, z);
-        }
-        // the block's share of dB and dC
-        for (int k = tid * 4; k < TC * 2 * S::N; k += kThreads * 4) {
-            const int tt = k / (2 * S::N), r = k % (2 * S::N);
-            if (t + tt >= w.t1) break;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t + tt < end)
+            put_steps<S>(sm.sd[f], pt, pc, d, x);
+            put_bc(sm.sb[f], rb, inb);
+            if (back) {
+                float g[S::EPT], z[S::EPT];
+                widen<T, S::EPT>(in_.y, g);
+                widen<T, S::EPT>(in_.z, z);
 #pragma unroll
-                for (int u = 0; u < kThreads / 32; ++u) {
-                    const float4 o = *reinterpret_cast<const float4 *>(&sm.bc[u][tt][0][0] + r);
-                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                for (int e = 0; e < S::EPT; ++e) {
+                    if (a.z) g[e] *= silu_f32(z[e]);
+                    g[e] = in[e] ? g[e] : 0.f;
                 }
-            *reinterpret_cast<float4 *>(a.part_bc + ((((long long)w.tile * a.B + w.b) * a.L + t + tt) * a.G + w.g) * (2 * S::N) + r) = v;
-        }
-        __syncthreads();
-    }
-
-    float *sums = a.part + (long long)(w.seg * a.B + w.b) * a.C * (S::N + 2);
-    if (on) {
-        if (w.seg == 0 && a.dh0) scatter<S>(a.dh0 + bc * S::N + n0, ox, p);
-        scatter<S>(sums + (long long)c * S::N + n0, ox, dA);
-    }
-    // dD and ddt_bias: over the tokens that each thread prepared
+                store_raw<float, S::EPT>(&sm.sg[f][pt][pc], narrow<float, S::EPT>(g));
+                put_bc(sm.sc[f], rc, inb);
+            }
+        };
+        const auto finish = [&](int i) {
+            const int t = w.t0 + i * TC, f = i & 1;
+            const bool in = t + pt < end;
+            if (t + pt < w.t1 && pc < w.nc) {
+                float x[S::EPT], v[S::EPT], y[S::EPT], z[S::EPT], g[S::EPT], q1[S::EPT], q2[S::EPT], q3[S::EPT];
+                widen<T, S::EPT>(old.x, x);
+                widen<T, S::EPT>(old.d, v);
+                widen<T, S::EPT>(old.y, y);
+                widen<T, S::EPT>(old.z, z);
+                widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.sg[f][pt][pc]), g);
+                widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s1[f][pt][pc]), q1);
+                widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s2[f][pt][pc]), q2);
+                widen<float, S::EPT>(load_raw<float, S::EPT>(&sm.s3[f][pt][pc]), q3);
 #pragma unroll
-    for (int e = 0; e < S::EPT; ++e) {
-        sm.s1[pt][pc + e] = aD[e];
-        sm.s2[pt][pc + e] = ab[e];
-    }
-    __syncthreads();
-    if (tid < w.nc) {
-        float u = 0.f, v = 0.f;
-        for (int tt = 0; tt < TC; ++tt) {
-            u += sm.s1[tt][tid];
-            v += sm.s2[tt][tid];
+                for (int e = 0; e < S::EPT; ++e) {
+                    const float d = sm.sd[f][pt][S::place(pc + e, pt)].x;
+                    q2[e] = fmaf(x[e], q1[e], q2[e]);
+                    if (a.softplus) q2[e] *= sigmoid_f32(v[e] + bias[e]);
+                    q1[e] = fmaf(d, q1[e], dskip[e] * g[e]);
+                    if (a.z) z[e] = y[e] * fmaf(dskip[e], x[e], q3[e]) * dsilu_f32(z[e]);
+                    q1[e] = in ? q1[e] : 0.f;
+                    q2[e] = in ? q2[e] : 0.f;
+                    z[e] = in ? z[e] : 0.f;
+                    ab[e] += q2[e];
+                    aD[e] += in ? g[e] * x[e] : 0.f;
+                }
+                const long long at = ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
+                const auto put = [&](void *to, const float(&o)[S::EPT]) {
+                    const Raw<T, S::EPT> r = narrow<T, S::EPT>(o);
+                    if constexpr (VEC) store_raw<T, S::EPT>(static_cast<T *>(to) + at, r);
+                    else store_raw_any<T, S::EPT>(static_cast<T *>(to) + at, r, w.nc - pc);
+                };
+                put(a.dx, q1);
+                put(a.ddt, q2);
+                if (a.z) put(a.dz, z);
+            }
+            // the block's share of dB and dC
+            for (int k = tid * 4; k < TC * 2 * S::N; k += kThreads * 4) {
+                const int tt = k / (2 * S::N), r = k % (2 * S::N);
+                if (t + tt >= w.t1) break;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t + tt < end)
+#pragma unroll
+                    for (int u = 0; u < kThreads / 32; ++u) {
+                        const float4 o = *reinterpret_cast<const float4 *>(&sm.bc[f][u][tt][0][0] + r);
+                        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                    }
+                *reinterpret_cast<float4 *>(a.part_bc + ((((long long)w.tile * a.B + w.b) * a.L + t + tt) * a.G + w.g) * (2 * S::N) + r) = v;
+            }
+        };
+        load(0, false);
+        prepare(0, false);
+        load(1, false);
+        tile_barrier();
+        for (int k = 0; k < tiles; ++k) {
+            if (k + 1 < tiles) prepare(k + 1, false);
+            load(k + 2, false);
+            tile_barrier();
         }
-        sums[(long long)a.C * S::N + w.c0 + tid] = u;
-        sums[(long long)a.C * (S::N + 1) + w.c0 + tid] = v;
+        load(all - 1, true);
+        prepare(all - 1, true);
+        mid = in_;
+        load(all - 2, true);
+        tile_barrier();
+        for (int i = all - 1; i >= 0; --i) {
+            if (i + 1 < all) finish(i + 1);  // reads D and g where the next line puts those of tile i - 1
+            if (i > 0) prepare(i - 1, true);
+            const Rows now = in_;
+            load(i - 2, true);
+            old = mid;
+            mid = now;
+            tile_barrier();
+        }
+        finish(0);
+        // dD and ddt_bias: over the tokens that each thread prepared
+        asm volatile("bar.sync 2, 128;" ::: "memory");  // every finish is done with s1 and s2
+#pragma unroll
+        for (int e = 0; e < S::EPT; ++e) {
+            sm.s1[0][pt][pc + e] = aD[e];
+            sm.s2[0][pt][pc + e] = ab[e];
+        }
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        if (tid < w.nc) {
+            float u = 0.f, v = 0.f;
+            for (int tt = 0; tt < TC; ++tt) {
+                u += sm.s1[0][tt][tid];
+                v += sm.s2[0][tt][tid];
+            }
+            sums[(long long)a.C * S::N + w.c0 + tid] = u;
+            sums[(long long)a.C * (S::N + 1) + w.c0 + tid] = v;
+        }
     }
 }
 
