@@ -1,7 +1,7 @@
 """Build the EFLA CUDA library in-tree: ``delta_rule_linear_03_b200/libefla.so``.
 
-Compiles ``csrc/efla_api.cu`` (the mixer) and ``csrc/efla_block_api.cu`` (the
-operators around it), which between them include every kernel header, side by
+Compiles ``csrc/efla_api.cu`` (the mixer), ``csrc/efla_block_api.cu`` (the
+operators around it) and ``csrc/efla_scan_*.cu`` (the scan's kernels), side by
 side for sm_100a only, and links them with the CUDA runtime, statically, so the
 library needs nothing but the driver at run time.  Rebuilds when any source under
 ``csrc/`` or ``include/`` is newer than the library.
@@ -24,7 +24,7 @@ SO = os.path.join(HERE, "libefla.so")
 SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu")) +
                  glob.glob(os.path.join(HERE, "csrc", "*.cuh")) +
                  glob.glob(os.path.join(ROOT, "include", "*.h")))
-UNITS = ("efla_api", "efla_block_api")
+UNITS = ("efla_api", "efla_block_api", "efla_scan_fwd_f32", "efla_scan_fwd_bf16", "efla_scan_bwd_f32", "efla_scan_bwd_bf16")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -4,12 +4,12 @@
 #include "efla_conv.cuh"
 #include "efla_host.cuh"
 #include "efla_norm.cuh"
-#include "efla_scan.cuh"
+#include "efla_scan_launch.cuh"
 
 using namespace efla;
 using namespace efla::host;
+using scan::rows_in_vectors;
 
-#include <cstdlib>
 namespace {
 
 // One buffer of a call: where it is, how many bytes from its first to its last.
@@ -150,59 +150,38 @@ efla_status_t check_conv(efla_dtype_t dtype, long long ldx, int B, int L, int C,
     return EFLA_OK;
 }
 
-// Whether rows can be read in vectors of `vec` elements.
-bool rows_in_vectors(const void *p, long long ld, int vec, size_t e) {
-    return aligned_to(p, std::min<size_t>(16, vec * e)) && ld % vec == 0;
-}
-
 // ---------------------------------------------------------------- scan
 
-struct ScanPlan {
-    int ns, cp;  // state values of a lane in each channel, channels of a lane
-    int nseg, seg, tpg;
-    long long blocks;  // of one segment
-    int sub() const { return ns * cp >= 8 ? 4 : 8; }  // tokens from one checkpoint of the backward pass to the next
-};
-
-constexpr int tile_channels(int N, int ns, int cp) { return scan::kThreads * ns / N * cp; }
-
-// How the work is cut.  Wide blocks (two channels a lane, eight state values
-// in all but N = 8) read least shared memory a value and are taken where they
-// give most SMs one; else a lane has one channel and two values (four of 64),
-// which makes four times as many blocks.  Where that still leaves most SMs
-// without one and the sequence is long, it is cut into segments of wide
-// blocks, which repeats the exponentials once (twice in the backward pass).
-ScanPlan scan_plan(int B, int L, int C, int G, int N, bool bwd) {
-    ScanPlan p;
+// How the work is cut.  A block's recurrence is four warps, one a scheduler,
+// which alone leaves most of its latencies open: PLAN_COMMENT
+scan::Plan scan_plan(int B, int L, int C, int G, int N, bool bwd) {
+    scan::Plan p;
     const int sms = num_sms(), cg = C / G;
+    // 0: one channel and two state values a lane (four of 64); 1: four; 2: two channels, four values each (two of 8)
     const auto shape = [&](int kind) {
         p.ns = N == 64 || (kind > 0 && !(N == 8 && kind == 2)) ? 4 : 2;
         p.cp = kind == 2 ? 2 : 1;
-        const int ct = tile_channels(N, p.ns, p.cp);
+        const int ct = scan::tile_channels(N, p.ns, p.cp);
         p.tpg = (cg + ct - 1) / ct;
         return p.blocks = (long long)B * G * p.tpg;
     };
     p.nseg = 1;
-    const long long wide = shape(2);
-    if (wide * 8 < sms * 5LL) {
-        if (shape(0) * 2 < sms) {
-            const long long want = 2LL * sms / std::max<long long>(1, wide), most = L / 128;
-            if (std::min(want, most) >= 3) {
-                shape(2);
-                p.nseg = (int)std::min<long long>(std::min(want, most), 64);
-            }
-        }
+    const long long two = shape(2), one = shape(1), zero = shape(0);
+    if (N == 64 ? two * 2 >= sms : two >= 3 * sms && !(bwd && N < 32)) {
+        shape(2);
+    } else if (one >= sms) {
+        shape(1);
+    } else if (zero * 3 < sms * (bwd ? 4LL : 2LL) && L >= 3 * 128) {
+        shape(1);
+        p.nseg = (int)std::max<long long>(1, std::min<long long>(4LL * sms / one, L / 128));
     }
-    (void)bwd;
-    if (getenv("T_WIDE")) shape(atoi(getenv("T_WIDE")));
-    if (getenv("T_SEG")) p.nseg = atoi(getenv("T_SEG"));
     const int seg = (L + p.nseg - 1) / p.nseg;
     p.seg = (seg + 31) / 32 * 32;  // 32: a multiple of every tile
     p.nseg = L > 0 ? (L + p.seg - 1) / p.seg : 1;
     return p;
 }
 
-size_t seg_floats(const ScanPlan &p, int B, int C, int N, bool bwd) {
+size_t seg_floats(const scan::Plan &p, int B, int C, int N, bool bwd) {
     if (p.nseg == 1) return 0;
     const size_t bc = (size_t)B * C;
     return bc * N * (p.nseg * (bwd ? 2 : 1) + 1) + round16(bc * p.nseg * 4) / 4;
@@ -227,7 +206,7 @@ struct BwdSizes {
     size_t seg, ckpt, bc, part;
     size_t bytes() const { return (seg + ckpt + bc + part) * sizeof(float); }
 };
-BwdSizes bwd_sizes(const ScanPlan &p, int B, int L, int C, int G, int N) {
+BwdSizes bwd_sizes(const scan::Plan &p, int B, int L, int C, int G, int N) {
     BwdSizes s;
     s.seg = seg_floats(p, B, C, N, true);
     s.ckpt = (size_t)p.blocks * p.nseg * (p.seg / p.sub()) * scan::kThreads * p.ns * p.cp;
@@ -248,74 +227,23 @@ efla_status_t check_scan(efla_dtype_t dtype, int B, int L, int C, int G, int N) 
     return EFLA_OK;
 }
 
-#define EFLA_SCAN_N(F, T, N, P, ...)                                                           \
-    do {                                                                                       \
-        if ((P).cp == 2) {                                                                     \
-            if ((N) == 8) return F<T, scan::Shape<8, 2, 2>>(__VA_ARGS__);                      \
-            if ((N) == 16) return F<T, scan::Shape<16, 4, 2>>(__VA_ARGS__);                    \
-            if ((N) == 32) return F<T, scan::Shape<32, 4, 2>>(__VA_ARGS__);                    \
-            return F<T, scan::Shape<64, 4, 2>>(__VA_ARGS__);                                   \
-        }                                                                                      \
-        if ((P).ns == 4) {                                                                     \
-            if ((N) == 8) return F<T, scan::Shape<8, 4, 1>>(__VA_ARGS__);                      \
-            if ((N) == 16) return F<T, scan::Shape<16, 4, 1>>(__VA_ARGS__);                    \
-            if ((N) == 32) return F<T, scan::Shape<32, 4, 1>>(__VA_ARGS__);                    \
-            return F<T, scan::Shape<64, 4, 1>>(__VA_ARGS__);                                   \
-        }                                                                                      \
-        if ((N) == 8) return F<T, scan::Shape<8, 2, 1>>(__VA_ARGS__);                          \
-        if ((N) == 16) return F<T, scan::Shape<16, 2, 1>>(__VA_ARGS__);                        \
-        return F<T, scan::Shape<32, 2, 1>>(__VA_ARGS__);                                       \
-    } while (0)
-
-template <typename T, typename S> bool scan_vec(const scan::Args &a) {
-    const size_t e = sizeof(T);
-    const int cg = a.C / a.G;
-    bool v = cg % S::EPT == 0;
-    for (const auto &q : {std::make_pair(a.x, a.ldx), std::make_pair(a.dt, a.lddt), std::make_pair(a.z, a.ldz)})
-        v = v && rows_in_vectors(q.first, q.second, S::EPT, e);
-    for (const auto &q : {std::make_pair(a.Bm, a.ldb), std::make_pair(a.Cm, a.ldc)})
-        v = v && rows_in_vectors(q.first, q.second, S::BPT, e);
-    return v;
-}
-
-template <typename T, typename S, bool VEC, scan::Mode MODE>
-efla_status_t run_scan(const scan::Args &a, unsigned grid, cudaStream_t st) {
-    constexpr size_t smem = sizeof(scan::FwdSmem<S>);
-    if (!ensure_smem<scan::scan_fwd_kernel<T, S, VEC, MODE>>(smem)) return EFLA_ERR_CUDA;
-    scan::scan_fwd_kernel<T, S, VEC, MODE><<<grid, 2 * scan::kThreads, smem, st>>>(a);
-    return launched();
-}
-
-template <typename T, typename S, bool VEC> efla_status_t run_scan_fwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
-    if (a.nseg > 1) {
-        const efla_status_t s = run_scan<T, S, VEC, scan::STATE>(a, grid, st);
+template <typename T> efla_status_t run_scan_fwd(const scan::Args &a, const scan::Plan &p, cudaStream_t st) {
+    if (p.nseg > 1) {
+        const efla_status_t s = scan::launch_forward<T>(scan::STATE, a, p, st);
         if (s != EFLA_OK) return s;
     }
-    return run_scan<T, S, VEC, scan::FULL>(a, grid, st);
+    return scan::launch_forward<T>(scan::FULL, a, p, st);
 }
 
-template <typename T, typename S> efla_status_t launch_scan_fwd(const scan::Args &a, long long blocks, cudaStream_t st) {
-    const unsigned grid = (unsigned)(blocks * a.nseg);
-    return scan_vec<T, S>(a) ? run_scan_fwd<T, S, true>(a, grid, st) : run_scan_fwd<T, S, false>(a, grid, st);
-}
-
-template <typename T, typename S, bool VEC> efla_status_t run_scan_bwd(const scan::Args &a, unsigned grid, cudaStream_t st) {
-    constexpr size_t smem = sizeof(scan::BwdSmem<S>);
-    if (!ensure_smem<scan::scan_bwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
-    if (a.nseg > 1) {
-        efla_status_t s = run_scan<T, S, VEC, scan::STATE>(a, grid, st);
-        if (s == EFLA_OK) s = run_scan<T, S, VEC, scan::BACK>(a, grid, st);
-        if (s != EFLA_OK) return s;
+template <typename T>
+efla_status_t run_scan_bwd(const scan::Args &a, const scan::Plan &p, void *dB, void *dC, float *dA, float *dD,
+                           float *db, cudaStream_t st) {
+    efla_status_t s = EFLA_OK;
+    if (p.nseg > 1) {
+        s = scan::launch_forward<T>(scan::STATE, a, p, st);
+        if (s == EFLA_OK) s = scan::launch_forward<T>(scan::BACK, a, p, st);
     }
-    scan::scan_bwd_kernel<T, S, VEC><<<grid, 2 * scan::kThreads, smem, st>>>(a);
-    return launched();
-}
-
-template <typename T, typename S>
-efla_status_t launch_scan_bwd(const scan::Args &a, long long blocks, void *dB, void *dC, float *dA, float *dD,
-                              float *db, cudaStream_t st) {
-    const unsigned grid = (unsigned)(blocks * a.nseg);
-    efla_status_t s = scan_vec<T, S>(a) ? run_scan_bwd<T, S, true>(a, grid, st) : run_scan_bwd<T, S, false>(a, grid, st);
+    if (s == EFLA_OK) s = scan::launch_backward<T>(a, p, st);
     if (s != EFLA_OK) return s;
     const long long rows = (long long)a.B * a.L * a.G, quads = rows * 2 * a.N / 4;
     scan::scan_bc_kernel<T><<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(a.part_bc, static_cast<T *>(dB),
@@ -561,7 +489,7 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
     if (!aligned_to(x, e) || !aligned_to(dt, e) || !aligned_to(Bm, e) || !aligned_to(Cm, e) || !aligned_to(z, e) ||
         !aligned_to(lengths, 4) || !all_aligned16({A, D, dt_bias, h0, y, h_L, workspace}))
         return EFLA_ERR_ALIGN;
-    const ScanPlan p = scan_plan(B, L, C, G, N, false);
+    const scan::Plan p = scan_plan(B, L, C, G, N, false);
     const size_t need = seg_floats(p, B, C, N, false) * sizeof(float);
     if (need && (!workspace || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
     const long long rows = (long long)B * L;
@@ -578,8 +506,7 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
     a.B = B; a.L = L; a.C = C; a.G = G; a.N = N; a.tpg = p.tpg; a.nseg = p.nseg; a.seg = p.seg;
     float *ws = static_cast<float *>(workspace);
     carve_segments(a, ws, false);
-    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_fwd, float, N, p, a, p.blocks, st);
-    EFLA_SCAN_N(launch_scan_fwd, __nv_bfloat16, N, p, a, p.blocks, st);
+    return dtype == EFLA_F32 ? run_scan_fwd<float>(a, p, st) : run_scan_fwd<__nv_bfloat16>(a, p, st);
 }
 
 size_t efla_scan_bwd_workspace_size(int B, int L, int C, int G, int N) {
@@ -618,7 +545,7 @@ efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const 
     if (!aligned_to(x, e) || !aligned_to(dt, e) || !aligned_to(Bm, e) || !aligned_to(Cm, e) || !aligned_to(z, e) ||
         !aligned_to(lengths, 4) || !all_aligned16({dy, A, D, dt_bias, h0, dx, ddt, dB, dC, dz, workspace}))
         return EFLA_ERR_ALIGN;
-    const ScanPlan p = scan_plan(B, L, C, G, N, true);
+    const scan::Plan p = scan_plan(B, L, C, G, N, true);
     const BwdSizes z4 = bwd_sizes(p, B, L, C, G, N);
     if (!workspace || workspace_bytes < z4.bytes()) return EFLA_ERR_WORKSPACE;
     const long long rows = (long long)B * L;
@@ -642,8 +569,8 @@ efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const 
     ws += z4.bc;
     carve_segments(a, ws, true);
     a.part = ws;
-    if (dtype == EFLA_F32) EFLA_SCAN_N(launch_scan_bwd, float, N, p, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
-    EFLA_SCAN_N(launch_scan_bwd, __nv_bfloat16, N, p, a, p.blocks, dB, dC, dA, dD, ddt_bias, st);
+    return dtype == EFLA_F32 ? run_scan_bwd<float>(a, p, dB, dC, dA, dD, ddt_bias, st)
+                             : run_scan_bwd<__nv_bfloat16>(a, p, dB, dC, dA, dD, ddt_bias, st);
 }
 
 efla_status_t efla_scan_step(const void *x, long long ldx, const void *dt, long long lddt, const float *A,

@@ -70,13 +70,12 @@ struct Args {
     float *dh0;
 };
 
-template <int N_, int NS_, int CP_> struct Shape {
-    static constexpr int N = N_, NS = NS_, CP = CP_;
+template <int N_, int NS_, int CP_, int TC_> struct Shape {
+    static constexpr int N = N_, NS = NS_, CP = CP_, TC = TC_;  // TC: tokens of a tile
     static constexpr int NP = NS / 2;                  // register pairs of a channel's state in a lane
     static constexpr int LN = N / NS;                  // lanes of a channel
     static constexpr int LC = 32 / LN;                 // channel groups (of CP) of a warp
     static constexpr int CT = kThreads / LN * CP;      // channels of a block
-    static constexpr int TC = CT > 32 || CP == 2 || N == 64 ? 16 : 32;  // tokens of a tile
     static constexpr int EPT = TC * CT / kThreads;     // neighbouring channels of one token that a thread prepares
     static constexpr int VPR = CT / EPT;               // threads a token's row takes
     static constexpr int BPT = TC * N / kThreads;      // values of B (and of C) that a thread loads
@@ -399,13 +398,14 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
                         }
                     }
                 };
-                float p[CP][TB];
+                // The sums stay in registers until the tile's end: a store between would keep the loads
+                // behind it from being issued ahead.
+                float p[CP][TB], done[TC / TB][CP];
                 const auto reduce = [&](int s) {
 #pragma unroll
-                    for (int i = 0; i < CP; ++i) halve<TB, 1, S::LN>(p[i], me.lane);
-                    if (S::LN <= TB || me.ln < TB) {
-                        if constexpr (CP == 2) *reinterpret_cast<float2 *>(out + s * S::CS) = make_float2(p[0][0], p[1][0]);
-                        else out[s * S::CS] = p[0][0];
+                    for (int i = 0; i < CP; ++i) {
+                        halve<TB, 1, S::LN>(p[i], me.lane);
+                        done[s / TB][i] = p[i][0];
                     }
                 };
                 terms(0, e[0], v[0]);
@@ -432,7 +432,15 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
                             if (MODE == FULL) p[i][(s + u) % TB] = sum2(y);
                         }
                 }
-                if (MODE == FULL) reduce(TC - TB);
+                if constexpr (MODE == FULL) {
+                    reduce(TC - TB);
+                    if (S::LN <= TB || me.ln < TB)
+#pragma unroll
+                        for (int s = 0; s < TC; s += TB) {
+                            if constexpr (CP == 2) *reinterpret_cast<float2 *>(out + s * S::CS) = make_float2(done[s / TB][0], done[s / TB][1]);
+                            else out[s * S::CS] = done[s / TB][0];
+                        }
+                }
             }
             tile_barrier();
         }
@@ -562,7 +570,9 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
 // and reads B and C from a copy in that order.
 
 template <typename S> struct BwdSmem {
-    static constexpr int COPY = S::TC * S::N + 16;  // one order's copy; the next begins 16 banks on
+    // One order's copy of B or C, so long that the copies which neighbouring lanes read at once lie in
+    // different banks (lanes of one access differ in the upper state bit first).
+    static constexpr int COPY = S::TC * S::N + (S::NS == 4 ? 8 : 16);
     alignas(16) float2 sd[2][S::TC][S::CT];         // D, D x
     alignas(16) float sg[2][S::TC][S::CS];          // g
     alignas(16) float s1[2][S::TC][S::CS];          // <p, B>
@@ -574,10 +584,10 @@ template <typename S> struct BwdSmem {
 };
 
 template <typename T, typename S, bool VEC>
-__global__ void __launch_bounds__(2 * kThreads) scan_bwd_kernel(Args a) {
+__global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2) scan_bwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     BwdSmem<S> &sm = *reinterpret_cast<BwdSmem<S> *>(raw_smem);
-    constexpr int NS = S::NS, NP = S::NP, LN = S::LN, TC = S::TC, TB = S::TB, CP = S::CP, SUB = NS * CP >= 8 ? 4 : 8;
+    constexpr int NS = S::NS, NP = S::NP, LN = S::LN, TC = S::TC, TB = S::TB, CP = S::CP, SUB = NS * CP >= 4 ? 4 : 8;
     constexpr int QB = TB < SUB ? TB : SUB;  // tokens whose sums over the state index are taken together
     const Where w(a, S::CT);
     const int end = min(w.t1, w.len);
@@ -681,9 +691,13 @@ __global__ void __launch_bounds__(2 * kThreads) scan_bwd_kernel(Args a) {
                                 hs[u + 1][i][j] = fma2(es[u][i][j], hs[u][i][j], mul2(d.u[i], b[j]));
                             }
                     }
+                    constexpr int SB = NS == 4 ? (S::LC >= 4 ? 2 : 1) : 1;  // state bits that are halved
+                    constexpr int V1 = 2 * NS >> SB, ST = LN << SB;          // what that leaves in a lane; the next lane bit
+                    // sums stay in registers until the end: a store between would keep the loads behind it
+                    // from being issued ahead
+                    float left[SUB][ST < 32 ? 1 : V1], q1[SUB / QB][CP][QB], q2[SUB / QB][CP][QB], q3[SUB / QB][CP][QB];
 #pragma unroll
                     for (int u0 = SUB - QB; u0 >= 0; u0 -= QB) {
-                        float q1[CP][QB], q2[CP][QB], q3[CP][QB];
 #pragma unroll
                         for (int r = QB - 1; r >= 0; --r) {
                             const int u = u0 + r;
@@ -723,9 +737,9 @@ __global__ void __launch_bounds__(2 * kThreads) scan_bwd_kernel(Args a) {
                                     y2 = j ? fma2(back, A1[i][j], y2) : mul2(back, A1[i][j]);
                                     part_dA[i][j] = fma2(back, d.d[i], part_dA[i][j]);
                                 }
-                                q1[i][r] = sum2(y1);
-                                q2[i][r] = sum2(y2);
-                                q3[i][r] = sum2(y3);
+                                q1[u0 / QB][i][r] = sum2(y1);
+                                q2[u0 / QB][i][r] = sum2(y2);
+                                q3[u0 / QB][i][r] = sum2(y3);
                             }
                             float m[2 * NS];  // of each register j: dB, dC
 #pragma unroll
@@ -737,36 +751,47 @@ __global__ void __launch_bounds__(2 * kThreads) scan_bwd_kernel(Args a) {
                                 m[4 * j + 3] = tc.y;
                             }
                             // over the channel lanes: first the state bits, by the lanes' orders, then dB from dC
-                            constexpr int SB = NS == 4 ? (S::LC >= 4 ? 2 : 1) : 1;  // state bits that are halved
-                            constexpr int V1 = 2 * NS >> SB, ST = LN << SB;
 #pragma unroll
                             for (int k = 0; k < NS; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS], LN);
                             if constexpr (SB == 2)
 #pragma unroll
                                 for (int k = 0; k < NS / 2; ++k) m[k] += __shfl_xor_sync(0xffffffffu, m[k + NS / 2], 2 * LN);
-                            // left: V1 / 2 states (registers 0 ..), dB and dC of each
                             if constexpr (ST < 32) {
                                 static_assert(V1 == 2, "one state is left where lanes are");
                                 halve<2, ST, 32>(m, lane);
-                                sm.bc[f][warp][s + u][(lane & ST) ? 1 : 0][n0 + ox] = m[0];
+                                left[u][0] = m[0];
                             } else {
 #pragma unroll
-                                for (int k = 0; k < V1; ++k) sm.bc[f][warp][s + u][k & 1][n0 + ((k >> 1) ^ ox)] = m[k];
+                                for (int k = 0; k < V1; ++k) left[u][k] = m[k];
                             }
                         }
-                        const int tt = s + u0 + halved_index<QB, 1, LN>(lane);
 #pragma unroll
                         for (int i = 0; i < CP; ++i) {
-                            halve<QB, 1, LN>(q1[i], lane);
-                            halve<QB, 1, LN>(q2[i], lane);
-                            if (a.z) halve<QB, 1, LN>(q3[i], lane);
-                            if (LN <= QB || me.ln < QB) {
-                                sm.s1[f][tt][me.cl + i] = q1[i][0];
-                                sm.s2[f][tt][me.cl + i] = q2[i][0];
-                                sm.s3[f][tt][me.cl + i] = q3[i][0];
-                            }
+                            halve<QB, 1, LN>(q1[u0 / QB][i], lane);
+                            halve<QB, 1, LN>(q2[u0 / QB][i], lane);
+                            if (a.z) halve<QB, 1, LN>(q3[u0 / QB][i], lane);
                         }
                     }
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        if constexpr (ST < 32) {
+                            sm.bc[f][warp][s + u][(lane & ST) ? 1 : 0][n0 + ox] = left[u][0];
+                        } else {  // V1 / 2 states (registers 0 ..), dB and dC of each
+#pragma unroll
+                            for (int k = 0; k < V1; ++k) sm.bc[f][warp][s + u][k & 1][n0 + ((k >> 1) ^ ox)] = left[u][k];
+                        }
+                    }
+                    if (LN <= QB || me.ln < QB)
+#pragma unroll
+                        for (int u0 = 0; u0 < SUB; u0 += QB) {
+                            const int tt = s + u0 + halved_index<QB, 1, LN>(lane);
+#pragma unroll
+                            for (int i = 0; i < CP; ++i) {
+                                sm.s1[f][tt][me.cl + i] = q1[u0 / QB][i][0];
+                                sm.s2[f][tt][me.cl + i] = q2[u0 / QB][i][0];
+                                sm.s3[f][tt][me.cl + i] = q3[u0 / QB][i][0];
+                            }
+                        }
                     // the long sum over tokens, with what its additions lose carried on
 #pragma unroll
                     for (int i = 0; i < CP; ++i)
