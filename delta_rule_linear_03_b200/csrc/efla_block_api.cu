@@ -415,13 +415,13 @@ efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_d
     a.part_w = static_cast<float *>(workspace);
     a.part_b = a.part_w + P * C * K;
     const int row = a.head ? a.head : C;
-    const bool vec = row % 4 == 0 && rows_in_vectors(x, ldx, 4, e);
-    const dim3 grid((unsigned)P, (unsigned)((C + 32 * (vec ? 4 : 1) - 1) / (32 * (vec ? 4 : 1))));
+    const bool vec = row % 2 == 0 && rows_in_vectors(x, ldx, 2, e);
+    const dim3 grid((unsigned)P, (unsigned)((C + 32 * (vec ? 2 : 1) - 1) / (32 * (vec ? 2 : 1))));
     if (dtype == EFLA_F32) {
-        if (vec) EFLA_CONV_K(conv::conv_bwd_kernel, float, 4, K, grid, 32 * conv::kWarps, a);
+        if (vec) EFLA_CONV_K(conv::conv_bwd_kernel, float, 2, K, grid, 32 * conv::kWarps, a);
         else EFLA_CONV_K(conv::conv_bwd_kernel, float, 1, K, grid, 32 * conv::kWarps, a);
     } else {
-        if (vec) EFLA_CONV_K(conv::conv_bwd_kernel, __nv_bfloat16, 4, K, grid, 32 * conv::kWarps, a);
+        if (vec) EFLA_CONV_K(conv::conv_bwd_kernel, __nv_bfloat16, 2, K, grid, 32 * conv::kWarps, a);
         else EFLA_CONV_K(conv::conv_bwd_kernel, __nv_bfloat16, 1, K, grid, 32 * conv::kWarps, a);
     }
     if (launched() != EFLA_OK) return EFLA_ERR_CUDA;

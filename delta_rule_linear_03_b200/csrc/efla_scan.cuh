@@ -91,16 +91,6 @@ template <int N_, int NS_, int CP_, int TC_> struct Shape {
     }
 };
 
-__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
-    const float2 t = unpack2(v);
-    return pack2(ex2(t.x), ex2(t.y));
-}
-__device__ __forceinline__ f32x2 rcp_2(f32x2 v) {
-    const float2 t = unpack2(v);
-    return pack2(rcp(t.x), rcp(t.y));
-}
-__device__ __forceinline__ f32x2 twice(float v) { return pack2(v, v); }
-
 // softplus(v) = max(v, 0) + log1p(e), e = e^-|v|, by log1p(e) = 2 atanh(s),
 // s = e / (2 + e) <= 1/3, whose series s + s^3/3 + ... + s^13/13 leaves less
 // than 2^-26 of it.  A step's error goes into every decay of its token, so e

@@ -84,12 +84,11 @@ __device__ __forceinline__ float rcp(float v) {
 // 1 / (1 + e^-v) and v / (1 + e^-v); where e^-v overflows they are 0 and -0.
 __device__ __forceinline__ float sigmoid_f32(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
 __device__ __forceinline__ float silu_f32(float v) { return v * sigmoid_f32(v); }
-// silu and its derivative s (1 + v (1 - s)), s = sigmoid(v), with 1 - s as
-// e^-v s.  Below -80 the derivative is under 2^-100 and given as 0, where
-// e^-v times 0 would be no number.
+// d silu(v) / dv = s + s v (1 - s), s = sigmoid(v); 1 - s loses what is under
+// 2^-24 of 1, which v makes no more than |v| such steps of the result.
 __device__ __forceinline__ float dsilu_f32(float v) {
-    const float e = ex2(-kLog2e * v), s = rcp(1.f + e);
-    return v < -80.f ? 0.f : s * fmaf(v * e, s, 1.f);
+    const float s = sigmoid_f32(v);
+    return fmaf(s, fmaf(-v, s, v), s);
 }
 
 // Two fp32 operations in one instruction, on a register pair.
@@ -122,6 +121,22 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 __device__ __forceinline__ float sum2(f32x2 v) {
     const float2 t = unpack2(v);
     return t.x + t.y;
+}
+
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return pack2(ex2(t.x), ex2(t.y));
+}
+__device__ __forceinline__ f32x2 rcp_2(f32x2 v) {
+    const float2 t = unpack2(v);
+    return pack2(rcp(t.x), rcp(t.y));
+}
+__device__ __forceinline__ f32x2 twice(float v) { return pack2(v, v); }
+__device__ __forceinline__ f32x2 sigmoid_2(f32x2 v) { return rcp_2(add2(twice(1.f), ex2_2(mul2(v, twice(-kLog2e))))); }
+__device__ __forceinline__ f32x2 silu_2(f32x2 v) { return mul2(v, sigmoid_2(v)); }
+__device__ __forceinline__ f32x2 dsilu_2(f32x2 v) {
+    const f32x2 s = sigmoid_2(v);
+    return fma2(s, fma2(mul2(v, twice(-1.f)), s, v), s);
 }
 
 // Column sums of partial results, in a fixed order: out[i] = sum_p part[p][i].
