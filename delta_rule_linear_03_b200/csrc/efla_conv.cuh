@@ -25,8 +25,8 @@ namespace efla {
 namespace conv {
 
 constexpr int kWarps = 4;
-constexpr int kAhead = 4;
-constexpr int kRunFwd = 32, kRunBwd = 32;  // tokens of one thread's run; multiples of kAhead
+constexpr int kAhead = 8;
+constexpr int kShortRun = 16, kLongRun = 128;  // tokens of one thread's run; multiples of kAhead
 
 struct Args {
     const void *x;
@@ -35,7 +35,7 @@ struct Args {
     const void *state;
     const int *lengths;
     int silu, head;  // head: channels of a head where y (or dy) is [B][H][L][head], 0 where it is [B][L][C]
-    int B, L, C, tiles;
+    int B, L, C, run, tiles;
     // forward
     void *y, *state_out;
     // backward
@@ -156,17 +156,22 @@ __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(Args a) {
     constexpr int U = kAhead, NE = Vals<VEC>::NE;
     const int b = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
     const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * VEC, warp = threadIdx.x >> 5;
-    const int t0 = (tile * kWarps + warp) * kRunFwd;
+    const int t0 = (tile * kWarps + warp) * a.run;
     if (c >= a.C || (t0 >= a.L && t0 > 0)) return;
     const int len = length_of(a, b);
     const T *x = static_cast<const T *>(a.x) + (long long)b * a.L * a.ldx + c;
     const T *st = a.state ? static_cast<const T *>(a.state) + (long long)b * (K - 1) * a.C + c : nullptr;
     const long long ldy = a.head ? a.head : a.C;
+    if (t0 >= len && t0 > 0) {  // padding alone
+        T *y = static_cast<T *>(a.y) + out_at(a, b, t0, c);
+        for (int t = t0; t < min(t0 + a.run, a.L); ++t, y += ldy) store_raw<T, VEC>(y, zero_raw<T, VEC>());
+        return;
+    }
 
     Vals<VEC> w[K], bias, win[K - 1 + U];  // win: the K-1 inputs before a batch, and the batch
     load_filters<K, VEC>(a, c, w, bias);
     load_window<T, K, VEC>(a, x, st, t0, len, win);
-    const int t1 = min(t0 + kRunFwd, a.L), tl = min(t1, len);
+    const int t1 = min(t0 + a.run, a.L), tl = min(t1, len);
     const auto walk = [&](auto whole) {  // whole: every token of the run counts
         constexpr bool kWhole = decltype(whole)::value;
         const T *in = x + t0 * a.ldx;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(Args a) {
             for (int j = 0; j < K - 1; ++j) win[j] = win[j + U];
         }
     };
-    if (t0 + kRunFwd <= len) walk(Yes{});
+    if (t0 + a.run <= len) walk(Yes{});
     else walk(No{});
 
     if (a.state_out && t0 == 0) {
@@ -233,12 +238,15 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
     const int b = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (blockIdx.y * 32 + lane) * VEC;
-    const int t0 = (tile * kWarps + warp) * kRunBwd;
+    const int t0 = (tile * kWarps + warp) * a.run;
     Vals<VEC> dw[K], db = none<VEC>();
 #pragma unroll
     for (int j = 0; j < K; ++j) dw[j] = none<VEC>();
-    if (c < a.C && (t0 < a.L || t0 == 0)) {
-        const int len = length_of(a, b);
+    const int len = length_of(a, b);
+    if (c < a.C && t0 >= len && t0 > 0) {  // padding alone
+        T *dx = static_cast<T *>(a.dx) + ((long long)b * a.L + t0) * a.C + c;
+        for (int t = t0; t < min(t0 + a.run, a.L); ++t, dx += a.C) store_raw<T, VEC>(dx, zero_raw<T, VEC>());
+    } else if (c < a.C) {
         const T *x = static_cast<const T *>(a.x) + (long long)b * a.L * a.ldx + c;
         const T *st = a.state ? static_cast<const T *>(a.state) + (long long)b * (K - 1) * a.C + c : nullptr;
         const T *dso = a.dstate_out ? static_cast<const T *>(a.dstate_out) + (long long)b * (K - 1) * a.C + c : nullptr;
@@ -250,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
         load_window<T, K, VEC>(a, x, st, t0, len, win);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) d[j] = none<VEC>();
-        const int tl = min(t0 + kRunBwd + K - 1, len);
+        const int tl = min(t0 + a.run + K - 1, len);
         const T *in = x + t0 * a.ldx, *dy = static_cast<const T *>(a.dy) + out_at(a, b, t0, c);
         T *dx = static_cast<T *>(a.dx) + ((long long)b * a.L + t0 - (K - 1)) * a.C + c;  // of token t - (K-1)
         Raw<T, VEC> nx[U], ny[U];
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
                 win[K - 1 + u] = vals<T, VEC>(nx[u]);
                 d[K - 1 + u] = vals<T, VEC>(ny[u]);
             }
-            if (t + U < t0 + kRunBwd + K - 1) {
+            if (t + U < t0 + a.run + K - 1) {
                 if (t + 2 * U <= tl) load(t + U, Yes{});
                 else load(t + U, No{});
             }
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
                     }
                 }
                 if (!kInside && tt >= len) dn = none<VEC>();
-                if (kInside || tt < t0 + kRunBwd)
+                if (kInside || tt < t0 + a.run)
 #pragma unroll
                     for (int i = 0; i < NE; ++i) {
                         db.v[i] = plus(db.v[i], dn.v[i]);
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
                 }
                 if (kInside) {
                     store_raw<T, VEC>(dx, raw<T, VEC>(o));
-                } else if (to < a.L && to < t0 + kRunBwd && (to >= t0 || (to < 0 && t0 == 0))) {
+                } else if (to < a.L && to < t0 + a.run && (to >= t0 || (to < 0 && t0 == 0))) {
                     const int at = to - len + K - 1;  // the row of state_out that holds x_to
                     if (dso && at >= 0 && at < K - 1) {
                         const Vals<VEC> g = vals<T, VEC>(load_raw<T, VEC>(dso + (long long)at * a.C));
@@ -329,9 +337,9 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
             }
         };
         load(t0, No{});
-        for (int t = t0; t < t0 + kRunBwd + K - 1; t += U) {
+        for (int t = t0; t < t0 + a.run + K - 1; t += U) {
             // the first batch completes tokens before the run, the last those behind it; state_out's rows end at len
-            if (t >= t0 + K - 1 && t + U <= t0 + kRunBwd && t + U <= len - (K - 1)) batch(t, Yes{});
+            if (t >= t0 + K - 1 && t + U <= t0 + a.run && t + U <= len - (K - 1)) batch(t, Yes{});
             else batch(t, No{});
         }
     }
