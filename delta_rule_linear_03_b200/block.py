@@ -21,7 +21,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dt, _lib
+from . import EFLA_BF16, EFLA_F32, _check, _lib
 
 _p, _i, _l, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
 _lib.efla_norm_fwd.argtypes = [_p, _i, _p, _i, _p, _f, _p, _p, _p, _i, _p, _l, _i, _p]
@@ -46,49 +46,53 @@ for _name in ("norm_fwd", "norm_bwd", "conv_fwd", "conv_bwd", "conv_step", "scan
     getattr(_lib, "efla_" + _name).restype = _i
 
 _F32 = torch.float32
-_ACT = (torch.float32, torch.bfloat16)
+_CODE = {torch.float32: EFLA_F32, torch.bfloat16: EFLA_BF16}
+# current_stream() and current_device() build objects and check initialisation: several microseconds that a
+# one-token step does not have.  A tensor on the device is proof of the latter.
+_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _refuse(t, shape, dtype, dev, name):
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, as the first argument is")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _want(t, shape, dtype, dev, name):
     """A contiguous tensor of this shape, type and device, or None."""
-    if t is None:
-        return
-    if tuple(t.shape) != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, as the first argument is")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t is not None and (t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+        _refuse(t, shape, dtype, dev, name)
 
 
 def _act(t, name):
-    """Device and type of the activation that the others are held to."""
+    """Device index and type of the activation that the others are held to."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _ACT:
+    if t.dtype not in _CODE:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return t.device, t.dtype
+    return t.get_device(), t.dtype
 
 
-def _rows(t, lead, tail, dtype, dev, name):
-    """Elements from one token to the next of a [*lead, *tail] tensor: each
-    token's values are contiguous, and the tokens evenly spaced."""
-    if tuple(t.shape) != lead + tail or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {list(lead + tail)}, got {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, as the first argument is")
+def _rows(t, shape, lead, dtype, dev, name):
+    """Elements from one token to the next of a tensor whose first ``lead``
+    dimensions count tokens: each token's values are contiguous, and the
+    tokens evenly spaced."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, shape, dtype, dev, name)
     width = 1
-    for n in tail:
+    for n in shape[lead:]:
         width *= n
     if t.is_contiguous():
         return width
-    shape, stride = t.shape, t.stride()
+    stride = t.stride()
     step, ld = 1, None
-    for i in range(t.dim() - 1, len(lead) - 1, -1):  # inside a token
+    for i in range(len(shape) - 1, lead - 1, -1):  # inside a token
         if shape[i] != 1 and stride[i] != step:
             raise ValueError(f"the values of one token of {name} must be contiguous")
         step *= shape[i]
-    for i in range(len(lead) - 1, -1, -1):  # from token to token
+    for i in range(lead - 1, -1, -1):  # from token to token
         if shape[i] == 1:
             continue
         if ld is None:
@@ -106,26 +110,25 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, dev, where, *args):
+def _call(fn, dev, *args):
     """Call with the current stream of the tensors' device, made current if it is not."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, stream)
+    if _get_device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, stream)
+            status = fn(*args, _raw_stream(dev))
     if status:
-        _check(status, where)
+        _check(status, fn.__name__)
 
 
-def _scratch(need, workspace, dev):
-    """(workspace, its bytes): the caller's where it is large enough, else a new one."""
+def _scratch(need, workspace, x):
+    """(workspace, its bytes): the caller's where it is large enough, else a new one on x's device."""
     if not need:
         return None, 0
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        return torch.empty(need, dtype=torch.uint8, device=dev), need
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
+        return x.new_empty(need, dtype=torch.uint8), need
+    if workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {x.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -140,7 +143,7 @@ def norm_fwd(x, weight, residual=None, eps: float = 1e-6, out8: bool = False, gr
     the residual's dtype (x's, or float32), None without a residual; it may be
     passed as ``residual`` itself, to update the stream in place."""
     dev, T = _act(x, "x")
-    shape = tuple(x.shape)
+    shape = x.shape
     if not shape:
         raise ValueError("x must have a last dimension to norm over")
     C = shape[-1]
@@ -148,7 +151,7 @@ def norm_fwd(x, weight, residual=None, eps: float = 1e-6, out8: bool = False, gr
     _want(x, shape, T, dev, "x")
     _want(weight, (C,), _F32, dev, "weight")
     if residual is not None:
-        if residual.dtype != T and residual.dtype != _F32:
+        if residual.dtype is not T and residual.dtype is not _F32:
             raise TypeError(f"residual must be float32 or {T}, got {residual.dtype}")
         _want(residual, shape, residual.dtype, dev, "residual")
         if res_out is None:
@@ -161,19 +164,19 @@ def norm_fwd(x, weight, residual=None, eps: float = 1e-6, out8: bool = False, gr
         raise ValueError("group must be 128 or 0")
     Y = torch.float8_e4m3fn if out8 else T
     if y is None:
-        y = torch.empty(shape, dtype=Y, device=dev)
+        y = x.new_empty(shape, dtype=Y)
     else:
         _want(y, shape, Y, dev, "y")
     if out8:
         groups = shape[:-1] + ((C + 127) // 128 if group else 1,)
         if scale is None:
-            scale = torch.empty(groups, dtype=_F32, device=dev)
+            scale = x.new_empty(groups, dtype=_F32)
         else:
             _want(scale, groups, _F32, dev, "scale")
     elif scale is not None:
         raise ValueError("scale is written with out8 only")
-    _call(_lib.efla_norm_fwd, dev, "efla_norm_fwd", x.data_ptr(), _dt(x), _at(residual),
-          _dt(x) if residual is None else _dt(residual), weight.data_ptr(), eps, None if out8 else y.data_ptr(),
+    _call(_lib.efla_norm_fwd, dev, x.data_ptr(), _CODE[T], _at(residual),
+          _CODE[T if residual is None else residual.dtype], weight.data_ptr(), eps, None if out8 else y.data_ptr(),
           y.data_ptr() if out8 else None, _at(scale), group, _at(res_out), rows, C)
     return y, scale, res_out
 
@@ -184,22 +187,22 @@ def norm_bwd(dy, h, weight, dres_out=None, eps: float = 1e-6, workspace=None):
     (dx, dres, dweight): the gradient of x in dy's dtype and of the residual in
     h's - one tensor where the dtypes agree - and of the weight in float32."""
     dev, T = _act(dy, "dy")
-    shape = tuple(dy.shape)
+    shape = dy.shape
     if not shape:
         raise ValueError("dy must have a last dimension")
     C = shape[-1]
     rows = dy.numel() // C if C else 0
-    if h.dtype != T and h.dtype != _F32:
+    if h.dtype is not T and h.dtype is not _F32:
         raise TypeError(f"h must be float32 or {T}, got {h.dtype}")
     _want(dy, shape, T, dev, "dy")
     _want(h, shape, h.dtype, dev, "h")
     _want(dres_out, shape, h.dtype, dev, "dres_out")
     _want(weight, (C,), _F32, dev, "weight")
-    dx = torch.empty(shape, dtype=T, device=dev)
-    dres = dx if h.dtype == T else torch.empty(shape, dtype=h.dtype, device=dev)
-    dw = torch.empty(C, dtype=_F32, device=dev)
-    ws, n = _scratch(_lib.efla_norm_bwd_workspace_size(rows, C), workspace, dev)
-    _call(_lib.efla_norm_bwd, dev, "efla_norm_bwd", dy.data_ptr(), _dt(dy), h.data_ptr(), _dt(h), weight.data_ptr(), eps,
+    dx = torch.empty_like(dy)
+    dres = dx if h.dtype is T else torch.empty_like(h)
+    dw = dy.new_empty(C, dtype=_F32)
+    ws, n = _scratch(_lib.efla_norm_bwd_workspace_size(rows, C), workspace, dy)
+    _call(_lib.efla_norm_bwd, dev, dy.data_ptr(), _CODE[T], h.data_ptr(), _CODE[h.dtype], weight.data_ptr(), eps,
           _at(dres_out), dx.data_ptr(), None if dres is dx else dres.data_ptr(), dw.data_ptr(), rows, C, _at(ws), n)
     return dx, dres, dw
 
@@ -212,7 +215,7 @@ def _conv_args(x, weight, bias, state, lengths, heads):
         raise ValueError("x must be [B,L,C] and weight [C,K]")
     B, L, C = x.shape
     K = weight.shape[1]
-    ldx = _rows(x, (B, L), (C,), T, dev, "x")
+    ldx = _rows(x, x.shape, 2, T, dev, "x")
     _want(weight, (C, K), _F32, dev, "weight")
     _want(bias, (C,), _F32, dev, "bias")
     _want(state, (B, K - 1, C), T, dev, "state")
@@ -231,14 +234,14 @@ def conv_fwd(x, weight, bias=None, state=None, lengths=None, silu: bool = True, 
     ``state_out=state`` updates it in place)."""
     dev, T, B, L, C, K, ldx, out = _conv_args(x, weight, bias, state, lengths, heads)
     if y is None:
-        y = torch.empty(out, dtype=T, device=dev)
+        y = x.new_empty(out)
     else:
         _want(y, out, T, dev, "y")
     if state_out is not None:
         _want(state_out, (B, K - 1, C), T, dev, "state_out")
     elif want_state:
-        state_out = torch.empty((B, K - 1, C), dtype=T, device=dev)
-    _call(_lib.efla_conv_fwd, dev, "efla_conv_fwd", x.data_ptr(), ldx, _dt(x), weight.data_ptr(), _at(bias), _at(state),
+        state_out = x.new_empty((B, K - 1, C))
+    _call(_lib.efla_conv_fwd, dev, x.data_ptr(), ldx, _CODE[T], weight.data_ptr(), _at(bias), _at(state),
           _at(lengths), silu, y.data_ptr(), heads, _at(state_out), B, L, C, K)
     return y, state_out
 
@@ -251,12 +254,12 @@ def conv_bwd(dy, x, weight, bias=None, state=None, lengths=None, silu: bool = Tr
     dev, T, B, L, C, K, ldx, out = _conv_args(x, weight, bias, state, lengths, heads)
     _want(dy, out, T, dev, "dy")
     _want(dstate_out, (B, K - 1, C), T, dev, "dstate_out")
-    dx = torch.empty((B, L, C), dtype=T, device=dev)
-    dw = torch.empty((C, K), dtype=_F32, device=dev)
-    db = None if bias is None else torch.empty(C, dtype=_F32, device=dev)
-    ds = None if state is None else torch.empty((B, K - 1, C), dtype=T, device=dev)
-    ws, n = _scratch(_lib.efla_conv_bwd_workspace_size(B, L, C, K), workspace, dev)
-    _call(_lib.efla_conv_bwd, dev, "efla_conv_bwd", dy.data_ptr(), x.data_ptr(), ldx, _dt(x), weight.data_ptr(),
+    dx = x.new_empty((B, L, C))
+    dw = x.new_empty((C, K), dtype=_F32)
+    db = None if bias is None else x.new_empty(C, dtype=_F32)
+    ds = None if state is None else x.new_empty((B, K - 1, C))
+    ws, n = _scratch(_lib.efla_conv_bwd_workspace_size(B, L, C, K), workspace, x)
+    _call(_lib.efla_conv_bwd, dev, dy.data_ptr(), x.data_ptr(), ldx, _CODE[T], weight.data_ptr(),
           _at(bias), _at(state), _at(lengths), silu, heads, _at(dstate_out), dx.data_ptr(), dw.data_ptr(), _at(db),
           _at(ds), B, L, C, K, _at(ws), n)
     return dx, dw, db, ds
@@ -269,17 +272,17 @@ def conv_step(x, state, weight, bias=None, silu: bool = True, y=None):
         raise ValueError("x must be [B,C] and weight [C,K]")
     B, C = x.shape
     K = weight.shape[1]
-    ldx = _rows(x, (B,), (C,), T, dev, "x")
+    ldx = _rows(x, x.shape, 1, T, dev, "x")
     _want(weight, (C, K), _F32, dev, "weight")
     _want(bias, (C,), _F32, dev, "bias")
     if state is None:
         raise ValueError("state must be given")
     _want(state, (B, K - 1, C), T, dev, "state")
     if y is None:
-        y = torch.empty((B, C), dtype=T, device=dev)
+        y = x.new_empty((B, C))
     else:
         _want(y, (B, C), T, dev, "y")
-    _call(_lib.efla_conv_step, dev, "efla_conv_step", x.data_ptr(), ldx, _dt(x), state.data_ptr(), weight.data_ptr(),
+    _call(_lib.efla_conv_step, dev, x.data_ptr(), ldx, _CODE[T], state.data_ptr(), weight.data_ptr(),
           _at(bias), silu, y.data_ptr(), B, C, K)
     return y
 
@@ -292,11 +295,12 @@ def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lengths, lead):
     k = len(lead)
     if x.dim() != k + 1 or A.dim() != 2 or Bm.dim() != k + 2:
         raise ValueError(f"x must be [{','.join(lead)},C], A [C,N] and Bm [{','.join(lead)},G,N]")
-    head = tuple(x.shape[:k])
-    C, N, G = x.shape[k], A.shape[1], Bm.shape[k]
-    ld = [_rows(x, head, (C,), T, dev, "x"), _rows(dt, head, (C,), T, dev, "dt"),
-          _rows(Bm, head, (G, N), T, dev, "Bm"), _rows(Cm, head, (G, N), T, dev, "Cm"),
-          C if z is None else _rows(z, head, (C,), T, dev, "z")]
+    shape = x.shape
+    head = shape[:k]
+    C, N, G = shape[k], A.shape[1], Bm.shape[k]
+    bc = head + (G, N)
+    ld = (_rows(x, shape, k, T, dev, "x"), _rows(dt, shape, k, T, dev, "dt"), _rows(Bm, bc, k, T, dev, "Bm"),
+          _rows(Cm, bc, k, T, dev, "Cm"), C if z is None else _rows(z, shape, k, T, dev, "z"))
     _want(A, (C, N), _F32, dev, "A")
     _want(D, (C,), _F32, dev, "D")
     _want(dt_bias, (C,), _F32, dev, "dt_bias")
@@ -323,16 +327,16 @@ def scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, lengths=No
     dev, T, (B, L), C, G, N, ld = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lengths, ("B", "L"))
     _want(h0, (B, C, N), _F32, dev, "h0")
     if y is None:
-        y = torch.empty((B, L, C), dtype=T, device=dev)
+        y = x.new_empty((B, L, C))
     else:
         _want(y, (B, L, C), T, dev, "y")
     if h_L is not None:
         _want(h_L, (B, C, N), _F32, dev, "h_L")
     elif want_state:
-        h_L = torch.empty((B, C, N), dtype=_F32, device=dev)
-    ws, n = _scratch(_lib.efla_scan_fwd_workspace_size(B, L, C, G, N), workspace, dev)
-    _call(_lib.efla_scan_fwd, dev, "efla_scan_fwd", x.data_ptr(), ld[0], dt.data_ptr(), ld[1], A.data_ptr(),
-          Bm.data_ptr(), ld[2], Cm.data_ptr(), ld[3], _at(D), _at(z), ld[4], _at(dt_bias), _at(h0), _at(lengths), _dt(x),
+        h_L = x.new_empty((B, C, N), dtype=_F32)
+    ws, n = _scratch(_lib.efla_scan_fwd_workspace_size(B, L, C, G, N), workspace, x)
+    _call(_lib.efla_scan_fwd, dev, x.data_ptr(), ld[0], dt.data_ptr(), ld[1], A.data_ptr(),
+          Bm.data_ptr(), ld[2], Cm.data_ptr(), ld[3], _at(D), _at(z), ld[4], _at(dt_bias), _at(h0), _at(lengths), _CODE[T],
           softplus, y.data_ptr(), _at(h_L), B, L, C, G, N, _at(ws), n)
     return y, h_L
 
@@ -346,18 +350,17 @@ def scan_bwd(dy, x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, length
     _want(h0, (B, C, N), _F32, dev, "h0")
     _want(dh_L, (B, C, N), _F32, dev, "dh_L")
     _want(dy, (B, L, C), T, dev, "dy")
-    act, bc, f32 = dict(dtype=T, device=dev), (B, L, G, N), dict(dtype=_F32, device=dev)
-    dx, ddt = torch.empty((B, L, C), **act), torch.empty((B, L, C), **act)
-    dB, dC = torch.empty(bc, **act), torch.empty(bc, **act)
-    dz = None if z is None else torch.empty((B, L, C), **act)
-    dA = torch.empty((C, N), **f32)
-    dD = None if D is None else torch.empty(C, **f32)
-    db = None if dt_bias is None else torch.empty(C, **f32)
-    dh0 = torch.empty((B, C, N), **f32)
-    ws, n = _scratch(_lib.efla_scan_bwd_workspace_size(B, L, C, G, N), workspace, dev)
-    _call(_lib.efla_scan_bwd, dev, "efla_scan_bwd", dy.data_ptr(), x.data_ptr(), ld[0], dt.data_ptr(), ld[1],
+    dx, ddt = x.new_empty((B, L, C)), x.new_empty((B, L, C))
+    dB, dC = x.new_empty((B, L, G, N)), x.new_empty((B, L, G, N))
+    dz = None if z is None else x.new_empty((B, L, C))
+    dA = x.new_empty((C, N), dtype=_F32)
+    dD = None if D is None else x.new_empty(C, dtype=_F32)
+    db = None if dt_bias is None else x.new_empty(C, dtype=_F32)
+    dh0 = x.new_empty((B, C, N), dtype=_F32)
+    ws, n = _scratch(_lib.efla_scan_bwd_workspace_size(B, L, C, G, N), workspace, x)
+    _call(_lib.efla_scan_bwd, dev, dy.data_ptr(), x.data_ptr(), ld[0], dt.data_ptr(), ld[1],
           A.data_ptr(), Bm.data_ptr(), ld[2], Cm.data_ptr(), ld[3], _at(D), _at(z), ld[4], _at(dt_bias), _at(h0),
-          _at(lengths), _at(dh_L), _dt(x), softplus, dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(),
+          _at(lengths), _at(dh_L), _CODE[T], softplus, dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(),
           dC.data_ptr(), _at(dD), _at(dz), _at(db), _at(dh0), B, L, C, G, N, _at(ws), n)
     return dx, ddt, dA, dB, dC, dD, dz, db, dh0
 
@@ -370,10 +373,10 @@ def scan_step(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus: bool 
         raise ValueError("h must be given")
     _want(h, (B, C, N), _F32, dev, "h")
     if y is None:
-        y = torch.empty((B, C), dtype=T, device=dev)
+        y = x.new_empty((B, C))
     else:
         _want(y, (B, C), T, dev, "y")
-    _call(_lib.efla_scan_step, dev, "efla_scan_step", x.data_ptr(), ld[0], dt.data_ptr(), ld[1], A.data_ptr(),
-          Bm.data_ptr(), ld[2], Cm.data_ptr(), ld[3], _at(D), _at(z), ld[4], _at(dt_bias), _dt(x), softplus,
+    _call(_lib.efla_scan_step, dev, x.data_ptr(), ld[0], dt.data_ptr(), ld[1], A.data_ptr(),
+          Bm.data_ptr(), ld[2], Cm.data_ptr(), ld[3], _at(D), _at(z), ld[4], _at(dt_bias), _CODE[T], softplus,
           h.data_ptr(), y.data_ptr(), B, C, G, N)
     return y
