@@ -190,18 +190,29 @@ struct Where {
 };
 
 // EPT neighbouring channels, from channel pc on, of a row of nc; what lies past
-// the row's end repeats a channel of it.  VEC: pc and nc are multiples of EPT
-// and the row is aligned for whole vectors.  Rows are read whether or not
-// their token counts: a load without a condition can be issued a tile ahead.
-template <typename T, int EPT, bool VEC>
+// the row's end repeats a channel of it.  V: channels of one access, for which
+// rows are aligned and nc is a multiple (1: any row).  Rows are read whether
+// or not their token counts: a load without a condition can be issued a tile
+// ahead.
+template <typename T, int EPT, int V>
 __device__ __forceinline__ Raw<T, EPT> load_row(const T *row, int pc, int nc) {
-    if constexpr (VEC) {
-        return load_raw<T, EPT>(row + (pc < nc ? pc : 0));
-    } else {
-        Raw<T, EPT> r;
+    Raw<T, EPT> r;
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) r.e[i] = row[min(pc + i, nc - 1)];
-        return r;
+    for (int i = 0; i < EPT; i += V) {
+        const Raw<T, V> q = load_raw<T, V>(row + (pc + i < nc ? pc + i : 0));
+#pragma unroll
+        for (int j = 0; j < V; ++j) r.e[i + j] = q.e[j];
+    }
+    return r;
+}
+template <typename T, int EPT, int V>
+__device__ __forceinline__ void store_row(T *at, const float (&o)[EPT], int pc, int nc) {
+#pragma unroll
+    for (int i = 0; i < EPT; i += V) {
+        float q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[j] = o[i + j];
+        if (pc + i < nc) store_raw<T, V>(at + i, narrow<T, V>(q));
     }
 }
 template <typename T, int BPT, bool VEC> __device__ __forceinline__ Raw<T, BPT> load_bc(const T *p) {
@@ -326,7 +337,7 @@ template <typename S> struct FwdSmem {
     alignas(16) float sb[2][S::TC][S::N], sc[2][S::TC][S::N];
 };
 
-template <typename T, typename S, bool VEC, Mode MODE>
+template <typename T, typename S, int V, Mode MODE>
 __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(raw_smem);
@@ -464,11 +475,11 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
         const auto load = [&](int k) {
             const int t = w.t0 + max(tile_of(k), 0) * TC;
             const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
-            rx = load_row<T, S::EPT, VEC>(px + row * ldx, pc, w.nc);
-            rd = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-            if (MODE != STATE) rz = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-            rb = load_bc<T, S::BPT, VEC>(pb + rowb * ldb);
-            if (MODE == FULL) rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+            rx = load_row<T, S::EPT, V>(px + row * ldx, pc, w.nc);
+            rd = load_row<T, S::EPT, V>(pd + row * a.lddt, pc, w.nc);
+            if (MODE != STATE) rz = load_row<T, S::EPT, V>(pz + row * ldz, pc, w.nc);
+            rb = load_bc<T, S::BPT, (V > 1)>(pb + rowb * ldb);
+            if (MODE == FULL) rc = load_bc<T, S::BPT, (V > 1)>(pq + rowb * a.ldc);
         };
         const auto prepare = [&](int k) {
             const int t = w.t0 + tile_of(k) * TC, f = k & 1;
@@ -517,8 +528,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
                 o[e] = t + pt < end ? o[e] : 0.f;
             }
             T *y = static_cast<T *>(a.y) + ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
-            if constexpr (VEC) store_raw<T, S::EPT>(y, narrow<T, S::EPT>(o));
-            else store_raw_any<T, S::EPT>(y, narrow<T, S::EPT>(o), w.nc - pc);
+            store_row<T, S::EPT, V>(y, o, pc, w.nc);
         };
         load(0);
         prepare(0);
@@ -573,7 +583,7 @@ template <typename S> struct BwdSmem {
     alignas(16) float bc[2][kThreads / 32][S::TC][2][S::N];  // a warp's sums over its channels
 };
 
-template <typename T, typename S, bool VEC>
+template <typename T, typename S, int V>
 __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2) scan_bwd_kernel(Args a) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     BwdSmem<S> &sm = *reinterpret_cast<BwdSmem<S> *>(raw_smem);
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2
                                 f32x2 y1 = 0ull, y2 = 0ull, y3 = 0ull;
                                 // Half a pair's channels may be none where rows are not whole vectors: those
                                 // add nothing, even beside an infinite B or C.
-                                const bool add = VEC || i == 0 || me.on[i];
+                                const bool add = V > 1 || i == 0 || me.on[i];
 #pragma unroll
                                 for (int j = 0; j < NP; ++j) {
                                     f32x2 &pj = p[i][j];
@@ -830,13 +840,13 @@ __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2
         const auto load = [&](int i, bool back) {
             const int t = w.t0 + max(i, 0) * TC;
             const long long row = (long long)w.b * a.L + min(t + pt, a.L - 1), rowb = (long long)w.b * a.L + min(t + part.bt, a.L - 1);
-            in_.x = load_row<T, S::EPT, VEC>(px + row * a.ldx, pc, w.nc);
-            in_.d = load_row<T, S::EPT, VEC>(pd + row * a.lddt, pc, w.nc);
-            rb = load_bc<T, S::BPT, VEC>(pb + rowb * a.ldb);
+            in_.x = load_row<T, S::EPT, V>(px + row * a.ldx, pc, w.nc);
+            in_.d = load_row<T, S::EPT, V>(pd + row * a.lddt, pc, w.nc);
+            rb = load_bc<T, S::BPT, (V > 1)>(pb + rowb * a.ldb);
             if (back) {
-                in_.y = load_row<T, S::EPT, VEC>(py + row * a.C, pc, w.nc);
-                in_.z = load_row<T, S::EPT, VEC>(pz + row * ldz, pc, w.nc);
-                rc = load_bc<T, S::BPT, VEC>(pq + rowb * a.ldc);
+                in_.y = load_row<T, S::EPT, V>(py + row * a.C, pc, w.nc);
+                in_.z = load_row<T, S::EPT, V>(pz + row * ldz, pc, w.nc);
+                rc = load_bc<T, S::BPT, (V > 1)>(pq + rowb * a.ldc);
             }
         };
         // B or C of the tile, zeros past the end, in every lane's order
@@ -863,7 +873,7 @@ __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2
             const bool inb = t + part.bt < end;
             bool in[S::EPT];
 #pragma unroll
-            for (int e = 0; e < S::EPT; ++e) in[e] = t + pt < end && pc + (VEC ? 0 : e) < w.nc;
+            for (int e = 0; e < S::EPT; ++e) in[e] = t + pt < end && pc + (e & -V) < w.nc;
             float x[S::EPT], d[S::EPT];
             widen<T, S::EPT>(in_.x, x);
             widen<T, S::EPT>(in_.d, d);
@@ -917,14 +927,9 @@ __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2
                     aD[e] += in ? g[e] * x[e] : 0.f;
                 }
                 const long long at = ((long long)w.b * a.L + t + pt) * a.C + w.c0 + pc;
-                const auto put = [&](void *to, const float(&o)[S::EPT]) {
-                    const Raw<T, S::EPT> r = narrow<T, S::EPT>(o);
-                    if constexpr (VEC) store_raw<T, S::EPT>(static_cast<T *>(to) + at, r);
-                    else store_raw_any<T, S::EPT>(static_cast<T *>(to) + at, r, w.nc - pc);
-                };
-                put(a.dx, q1);
-                put(a.ddt, q2);
-                if (a.z) put(a.dz, z);
+                store_row<T, S::EPT, V>(static_cast<T *>(a.dx) + at, q1, pc, w.nc);
+                store_row<T, S::EPT, V>(static_cast<T *>(a.ddt) + at, q2, pc, w.nc);
+                if (a.z) store_row<T, S::EPT, V>(static_cast<T *>(a.dz) + at, z, pc, w.nc);
             }
             // the block's share of dB and dC
             for (int k = tid * 4; k < TC * 2 * S::N; k += kThreads * 4) {

@@ -54,14 +54,21 @@ inline bool rows_in_vectors(const void *p, long long ld, int vec, size_t e) {
     return host::aligned_to(p, std::min<size_t>(16, vec * e)) && ld % vec == 0;
 }
 
-template <typename T, typename S> bool in_vectors(const Args &a) {
+// Channels of one access to a row of activations: a thread's EPT, four of
+// eight, or single ones (1), as the rows' alignment and the groups' width
+// allow.  The last also where a row of Bm or Cm is not aligned for whole vectors.
+template <typename T, typename S> int row_vector(const Args &a) {
     const size_t e = sizeof(T);
-    bool v = a.C / a.G % S::EPT == 0;
-    for (const auto &q : {std::make_pair(a.x, a.ldx), std::make_pair(a.dt, a.lddt), std::make_pair(a.z, a.ldz)})
-        v = v && rows_in_vectors(q.first, q.second, S::EPT, e);
     for (const auto &q : {std::make_pair(a.Bm, a.ldb), std::make_pair(a.Cm, a.ldc)})
-        v = v && rows_in_vectors(q.first, q.second, S::BPT, e);
-    return v;
+        if (!rows_in_vectors(q.first, q.second, S::BPT, e)) return 1;
+    for (int v = S::EPT; v > 1; v /= 2) {
+        if (v != S::EPT && v != 4) continue;
+        bool fits = a.C / a.G % v == 0;
+        for (const auto &q : {std::make_pair(a.x, a.ldx), std::make_pair(a.dt, a.lddt), std::make_pair(a.z, a.ldz)})
+            fits = fits && rows_in_vectors(q.first, q.second, v, e);
+        if (fits) return v;
+    }
+    return 1;
 }
 
 template <typename T> struct Forward {
@@ -71,19 +78,24 @@ template <typename T> struct Forward {
     const Plan &p;
     cudaStream_t st;
 
-    template <typename S, bool VEC, Mode MODE> efla_status_t launch() const {
+    template <typename S, int V, Mode MODE> efla_status_t launch() const {
         constexpr size_t smem = sizeof(FwdSmem<S>);
-        if (!ensure_smem<scan_fwd_kernel<T, S, VEC, MODE>>(smem)) return EFLA_ERR_CUDA;
-        scan_fwd_kernel<T, S, VEC, MODE><<<(unsigned)(p.blocks * p.nseg), 2 * kThreads, smem, st>>>(a);
+        if (!ensure_smem<scan_fwd_kernel<T, S, V, MODE>>(smem)) return EFLA_ERR_CUDA;
+        scan_fwd_kernel<T, S, V, MODE><<<(unsigned)(p.blocks * p.nseg), 2 * kThreads, smem, st>>>(a);
         return host::launched();
     }
+    template <typename S, Mode MODE> efla_status_t pick() const {
+        const int v = row_vector<T, S>(a);
+        if constexpr (S::EPT == 1) return launch<S, 1, MODE>();
+        else if (v == S::EPT) return launch<S, S::EPT, MODE>();
+        if constexpr (S::EPT > 4)
+            if (v == 4) return launch<S, 4, MODE>();
+        return launch<S, 1, MODE>();
+    }
     template <typename S> efla_status_t run() const {
-        const bool vec = in_vectors<T, S>(a);
-        if (mode == FULL) return vec ? launch<S, true, FULL>() : launch<S, false, FULL>();
-        if constexpr (S::NS == 4 && S::CP == 1) {  // the shape of segments
-            if (mode == STATE) return vec ? launch<S, true, STATE>() : launch<S, false, STATE>();
-            return vec ? launch<S, true, BACK>() : launch<S, false, BACK>();
-        }
+        if (mode == FULL) return pick<S, FULL>();
+        if constexpr (S::NS == 4 && S::CP == 1)  // the shape of segments
+            return mode == STATE ? pick<S, STATE>() : pick<S, BACK>();
         return EFLA_ERR_UNSUPPORTED;
     }
 };
@@ -94,14 +106,19 @@ template <typename T> struct Backward {
     const Plan &p;
     cudaStream_t st;
 
-    template <typename S, bool VEC> efla_status_t launch() const {
+    template <typename S, int V> efla_status_t launch() const {
         constexpr size_t smem = sizeof(BwdSmem<S>);
-        if (!ensure_smem<scan_bwd_kernel<T, S, VEC>>(smem)) return EFLA_ERR_CUDA;
-        scan_bwd_kernel<T, S, VEC><<<(unsigned)(p.blocks * p.nseg), 2 * kThreads, smem, st>>>(a);
+        if (!ensure_smem<scan_bwd_kernel<T, S, V>>(smem)) return EFLA_ERR_CUDA;
+        scan_bwd_kernel<T, S, V><<<(unsigned)(p.blocks * p.nseg), 2 * kThreads, smem, st>>>(a);
         return host::launched();
     }
     template <typename S> efla_status_t run() const {
-        return in_vectors<T, S>(a) ? launch<S, true>() : launch<S, false>();
+        const int v = row_vector<T, S>(a);
+        if constexpr (S::EPT == 1) return launch<S, 1>();
+        else if (v == S::EPT) return launch<S, S::EPT>();
+        if constexpr (S::EPT > 4)
+            if (v == 4) return launch<S, 4>();
+        return launch<S, 1>();
     }
 };
 

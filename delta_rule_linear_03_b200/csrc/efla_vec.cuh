@@ -16,13 +16,6 @@ template <typename T, int N> struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof
 template <typename T, int N> __device__ __forceinline__ Raw<T, N> load_raw(const T *p) {
     return *reinterpret_cast<const Raw<T, N> *>(p);
 }
-// Element accesses: any p, and the first n elements alone (the others are 0).
-template <typename T, int N> __device__ __forceinline__ Raw<T, N> load_raw_any(const T *p, int n) {
-    Raw<T, N> r;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.e[i] = i < n ? p[i] : from_f32<T>(0.f);
-    return r;
-}
 template <typename T, int N> __device__ __forceinline__ Raw<T, N> zero_raw() {
     Raw<T, N> r;
 #pragma unroll
@@ -61,12 +54,6 @@ template <typename T, int N> __device__ __forceinline__ Raw<T, N> narrow(const f
 template <typename T, int N> __device__ __forceinline__ void store_raw(T *p, const Raw<T, N> &r) {
     *reinterpret_cast<Raw<T, N> *>(p) = r;
 }
-template <typename T, int N> __device__ __forceinline__ void store_raw_any(T *p, const Raw<T, N> &r, int n) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) p[i] = r.e[i];
-}
-
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // 2^v and 1 / v, approximate (2 and 1 ulp); subnormals count as zeros.
