@@ -231,3 +231,17 @@ def test_scan_refuses(efla):
         efla.scan_fwd(s["x"], s["dt"], s["A"][:, :12].contiguous(), s["Bm"][..., :12].contiguous(), s["Cm"][..., :12].contiguous())
     with pytest.raises(efla.EflaError):
         efla.scan_fwd(**s, y=s["x"])
+
+
+@pytest.mark.parametrize("B,L,C,N", [(2, 90, 24, 16), (1, 40, 5000, 16), (1, 1000, 16, 64)])
+def test_scan_steps_of_zero_leave_the_state(efla, B, L, C, N):
+    """Tokens whose step underflows to 0, and padding, keep every bit of the state."""
+    s = R.scan_inputs(B, L, C, N, 1, F)
+    n = 33
+    cut = {k: (t[:, :n].contiguous() if k in ("x", "dt", "Bm", "Cm", "z") else t) for k, t in s.items()}
+    _, h = _fwd(efla, cut)
+    s["dt"][:, n:] = -300.0
+    _, h1 = _fwd(efla, s)
+    s["lengths"] = torch.full((B,), n, dtype=torch.int32)
+    y2, h2 = _fwd(efla, s)
+    assert torch.equal(h, h1) and torch.equal(h, h2) and not y2[:, n:].any()
