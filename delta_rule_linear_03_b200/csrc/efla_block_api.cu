@@ -265,13 +265,9 @@ efla_status_t run_scan_bwd(const scan::Args &a, const scan::Plan &p, void *dB, v
 }
 
 template <typename T, int N> efla_status_t launch_scan_step(scan::Args a, cudaStream_t st) {
-    a.vec = rows_in_vectors(a.Bm, a.ldb, 4, sizeof(T)) && rows_in_vectors(a.Cm, a.ldc, 4, sizeof(T));
-    const long long gx = ((long long)a.C * (N / 4) + 127) / 128;
-    // four sequences a thread once that still leaves 16 warps an SM
-    if (gx * a.B >= 16LL * num_sms())
-        scan::scan_step_kernel<T, N, 4><<<dim3((unsigned)gx, (a.B + 3) / 4), 128, 0, st>>>(a);
-    else
-        scan::scan_step_kernel<T, N, 1><<<dim3((unsigned)gx, a.B), 128, 0, st>>>(a);
+    a.vec = rows_in_vectors(a.Bm, a.ldb, 8, sizeof(T)) && rows_in_vectors(a.Cm, a.ldc, 8, sizeof(T));
+    const long long gx = ((long long)a.C * (N / 8) + 127) / 128;
+    scan::scan_step_kernel<T, N><<<dim3((unsigned)gx, a.B), 128, 0, st>>>(a);
     return launched();
 }
 

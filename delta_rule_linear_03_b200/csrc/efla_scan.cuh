@@ -52,7 +52,7 @@ struct Args {
     const int *lengths;
     void *y;
     float *h_L;
-    int softplus, vec;  // vec: scan_step_kernel reads B and C in vectors of four
+    int softplus, vec;  // vec: scan_step_kernel reads B and C in vectors
     int B, L, C, G, N;
     int tpg;            // channel tiles of a group
     int nseg, seg;      // segments, and tokens of one (a multiple of the tile)
@@ -131,13 +131,13 @@ __device__ __forceinline__ float softplus_f32(float v) { return unpack2(softplus
 template <int N> __device__ __forceinline__ void softplus_all(float (&v)[N]) {
     if constexpr (N == 1) {
         v[0] = softplus_f32(v[0]);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i + 1 < N; i += 2) {
-        const float2 t = unpack2(softplus_2(pack2(v[i], v[i + 1])));
-        v[i] = t.x;
-        v[i + 1] = t.y;
+        for (int i = 0; i < N; i += 2) {
+            const float2 t = unpack2(softplus_2(pack2(v[i], v[i + 1])));
+            v[i] = t.x;
+            v[i + 1] = t.y;
+        }
     }
 }
 
@@ -1015,60 +1015,47 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float *__restrict__ 
 }
 
 // ---------------------------------------------------------------- one token
-// Four state values a thread, the state read and written once.  HBM bound
-// (8 N bytes a channel); a thread takes ROWS sequences of the same channel,
-// so that A is loaded once for them and several states are in flight.
-template <typename T, int N, int ROWS>
-__global__ void __launch_bounds__(128) scan_step_kernel(Args a) {
-    constexpr int LN = N / 4;
-    const int i = blockIdx.x * 128 + threadIdx.x, c = i / LN, n0 = (i % LN) * 4;
+// The state is read and written once: HBM bound, 8 N bytes a channel.  A
+// thread has eight values of a channel's state: with four, the step's
+// softplus and the loads of single values weigh more (256 x 8192 x 16: 61 us
+// against 89, the state's bytes at the copy rate 41), with sixteen, or two
+// sequences, fewer threads are resident (69, 64).
+template <typename T, int N> __global__ void __launch_bounds__(128) scan_step_kernel(Args a) {
+    constexpr int NS = 8, LN = N / NS;
+    const int i = blockIdx.x * 128 + threadIdx.x, c = i / LN, n0 = (i % LN) * NS, b = blockIdx.y;
     const bool on = c < a.C;
-    const int b0 = blockIdx.y * ROWS;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f), h[ROWS];
-    float bias = 0.f, dskip = 0.f, xv[ROWS], dv[ROWS], zv[ROWS];
-    float4 bv[ROWS], cv[ROWS];
-    const int g = on ? c / (a.C / a.G) : 0;
-    const auto four = [&](const void *base, long long ld, int b) {
-        const T *p = static_cast<const T *>(base) + b * ld + g * N + n0;
-        return a.vec ? load4(p) : make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
-    };
+    float p = 0.f, x = 0.f, z = 0.f, dskip = 0.f;
     if (on) {
+        const int off = c / (a.C / a.G) * N + n0;
+        const auto eight = [&](const void *base, long long ld) {
+            const T *q = static_cast<const T *>(base) + b * ld + off;
+            return a.vec ? load_raw<T, NS>(q) : load_bc<T, NS, false>(q);
+        };
+        float *at = a.h_L + ((long long)b * a.C + c) * N + n0;
+        float h[NS], A[NS], bv[NS], cv[NS];
+        widen<float, NS>(load_raw<float, NS>(at), h);
+        widen<float, NS>(load_raw<float, NS>(a.A + (long long)c * N + n0), A);
+        widen<T, NS>(eight(a.Bm, a.ldb), bv);
+        widen<T, NS>(eight(a.Cm, a.ldc), cv);
+        x = to_f32(static_cast<const T *>(a.x)[b * a.ldx + c]);
+        if (a.z) z = to_f32(static_cast<const T *>(a.z)[b * a.ldz + c]);
+        if (a.D) dskip = a.D[c];
+        float d = to_f32(static_cast<const T *>(a.dt)[b * a.lddt + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+        if (a.softplus) d = softplus_f32(d);
+        const float u = d * x, e = d * kLog2e;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-            if (b0 + r < a.B) {
-                const int b = b0 + r;
-                h[r] = *reinterpret_cast<const float4 *>(a.h_L + ((long long)b * a.C + c) * N + n0);
-                xv[r] = to_f32(static_cast<const T *>(a.x)[b * a.ldx + c]);
-                dv[r] = to_f32(static_cast<const T *>(a.dt)[b * a.lddt + c]);
-                zv[r] = a.z ? to_f32(static_cast<const T *>(a.z)[b * a.ldz + c]) : 0.f;
-                bv[r] = four(a.Bm, a.ldb, b);
-                cv[r] = four(a.Cm, a.ldc, b);
-            }
-        A = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + n0);
-        bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-        dskip = a.D ? a.D[c] : 0.f;
+        for (int j = 0; j < NS; ++j) {
+            h[j] = fmaf(ex2(fmaf(e, A[j], kCentre)), h[j], u * bv[j]);
+            p = fmaf(h[j], cv[j], p);
+        }
+        store_raw<float, NS>(at, narrow<float, NS>(h));
     }
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int b = b0 + r;
-        float p = 0.f;
-        if (on && b < a.B) {
-            const float d = a.softplus ? softplus_f32(dv[r] + bias) : dv[r] + bias, u = d * xv[r], e = d * kLog2e;
-            float4 v;
-            v.x = fmaf(ex2(fmaf(e, A.x, kCentre)), h[r].x, u * bv[r].x);
-            v.y = fmaf(ex2(fmaf(e, A.y, kCentre)), h[r].y, u * bv[r].y);
-            v.z = fmaf(ex2(fmaf(e, A.z, kCentre)), h[r].z, u * bv[r].z);
-            v.w = fmaf(ex2(fmaf(e, A.w, kCentre)), h[r].w, u * bv[r].w);
-            *reinterpret_cast<float4 *>(a.h_L + ((long long)b * a.C + c) * N + n0) = v;
-            p = fmaf(v.x, cv[r].x, fmaf(v.y, cv[r].y, fmaf(v.z, cv[r].z, v.w * cv[r].w)));
-        }
-#pragma unroll
-        for (int o = LN / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-        if (on && b < a.B && n0 == 0) {
-            float y = fmaf(dskip, xv[r], p);
-            if (a.z) y *= silu_f32(zv[r]);
-            static_cast<T *>(a.y)[(long long)b * a.C + c] = from_f32<T>(y);
-        }
+    for (int o = LN / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+    if (on && n0 == 0) {
+        float y = fmaf(dskip, x, p);
+        if (a.z) y *= silu_f32(z);
+        static_cast<T *>(a.y)[(long long)b * a.C + c] = from_f32<T>(y);
     }
 }
 
