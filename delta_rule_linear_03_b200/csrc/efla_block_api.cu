@@ -107,7 +107,7 @@ template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdA
 
 // Blocks of the backward pass, each with a row of partial column sums: as
 // many as are resident at once, fewer where there are fewer rows.
-long long norm_bwd_blocks(long long rows) { return std::min<long long>(rows, 4LL * num_sms()); }
+long long norm_bwd_blocks(long long rows) { return std::min<long long>(rows, 2LL * num_sms()); }
 
 template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdArgs &a, bool vec, int blocks, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
@@ -119,7 +119,7 @@ template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdA
     }
     const int nvec = a.C / VEC;
 #define EFLA_L(TPR, IT) \
-    norm::norm_bwd_kernel<T, R, TPR, IT, (IT == 1 ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
+    norm::norm_bwd_kernel<T, R, TPR, IT, (IT == 1 || (IT == 2 && sizeof(T) == 4) ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
     EFLA_NORM_VEC(EFLA_L, T, nvec);
 #undef EFLA_L
     return launched();

@@ -256,15 +256,24 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_fwd_any_kernel(FwdA
     const bool on = row < a.rows;
     const T *x = static_cast<const T *>(a.x) + row * C;
     const R *res = a.res ? static_cast<const R *>(a.res) + row * C : nullptr;
-    float h[IT][4], ss[1] = {0.f};
+    // all loads before the first store: one behind a store would wait for it, as far as the compiler can tell
+    float h[IT][4], w[IT][4], ss[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < IT; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
             h[k][j] = on && c < C ? to_f32(x[c]) : 0.f;
-            if (res && on && c < C) h[k][j] += to_f32(res[c]);
+            w[k][j] = c < C ? a.w[c] : 0.f;
         }
+    if (res)
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
+                if (on && c < C) h[k][j] += to_f32(res[c]);
+            }
 #pragma unroll
     for (int k = 0; k < IT; ++k)
 #pragma unroll
@@ -282,7 +291,7 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_fwd_any_kernel(FwdA
                 continue;
             }
             if (a.res_out) static_cast<R *>(a.res_out)[row * C + c] = from_f32<R>(h[k][j]);
-            h[k][j] = h[k][j] * rstd * a.w[c];
+            h[k][j] = h[k][j] * rstd * w[k][j];
             if (a.y) static_cast<T *>(a.y)[row * C + c] = from_f32<T>(h[k][j]);
             top[0] = max_abs(top[0], h[k][j]);
         }
@@ -324,7 +333,7 @@ struct BwdArgs {
 // A persistent block keeps its columns' share of dw in registers over all of
 // its rows; the shares of its row slots meet in shared memory at the end.
 template <typename T, typename R, int TPR, int IT, int RPI>
-__global__ void __launch_bounds__(kThreadsOf<TPR>) norm_bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) norm_bwd_kernel(BwdArgs a) {
     constexpr int VEC = 16 / sizeof(T), NT = kThreadsOf<TPR>, SLOTS = NT / TPR;
     __shared__ RowReduce<TPR, 2 * RPI> rs[2];
     __shared__ float cols[SLOTS > 1 ? SLOTS : 1][SLOTS > 1 ? TPR * IT * VEC : 1];
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_bwd_kernel(BwdArgs a) {
 
 // Any width, as norm_fwd_any_kernel lays rows out.
 template <typename T, typename R, int WPR, int IT>
-__global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kThreadsOf<WPR * 32>, WPR <= 8 ? 2 : 1) norm_bwd_any_kernel(BwdArgs a) {
     constexpr int TPR = WPR * 32, NT = kThreadsOf<TPR>, SLOTS = NT / TPR;
     __shared__ RowReduce<TPR, 2> rs[2];
     __shared__ float cols[SLOTS > 1 ? SLOTS : 1][SLOTS > 1 ? WPR * IT * kGroup : 1];
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdA
     for (long long base = (long long)blockIdx.x * SLOTS; base < a.rows; base += (long long)gridDim.x * SLOTS, par ^= 1) {
         const long long row = base + slot;
         const bool on = row < a.rows;
-        float hv[IT][4], yv[IT][4], s[2] = {0.f, 0.f};
+        float hv[IT][4], yv[IT][4], rv[IT][4], s[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < IT; ++k)
 #pragma unroll
@@ -443,6 +452,7 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdA
                 const bool in = on && c < C;
                 hv[k][j] = in ? to_f32(h[row * C + c]) : 0.f;
                 yv[k][j] = in ? to_f32(dy[row * C + c]) : 0.f;
+                rv[k][j] = in && dr ? to_f32(dr[row * C + c]) : 0.f;
             }
 #pragma unroll
         for (int k = 0; k < IT; ++k)
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>) norm_bwd_any_kernel(BwdA
                 const int c = (k * WPR + wr) * kGroup + j * 32 + lane;
                 if (!on || c >= C) continue;
                 acc[k][j] = fmaf(yv[k][j], hv[k][j] * rstd, acc[k][j]);
-                const float d = fmaf(rstd, yv[k][j] * w[k][j] - hv[k][j] * m, dr ? to_f32(dr[row * C + c]) : 0.f);
+                const float d = fmaf(rstd, yv[k][j] * w[k][j] - hv[k][j] * m, rv[k][j]);
                 if (a.dx) static_cast<T *>(a.dx)[row * C + c] = from_f32<T>(d);
                 if (a.dres) static_cast<R *>(a.dres)[row * C + c] = from_f32<R>(d);
             }

@@ -50,7 +50,7 @@ def norm_bwd(so, **kw):
 
 def test_norm_bwd_refusals(so):
     assert norm_bwd(so, C=0) == 0
-    need = so.efla_norm_bwd_workspace_size(64, 256)
+    need = so.efla_norm_bwd_workspace_size(64, 256)  # a row of sums a block, at most two blocks an SM
     assert need == 64 * 256 * 4 and so.efla_norm_bwd_workspace_size(0, 256) == 0 == so.efla_norm_bwd_workspace_size(4, 16385)
     for kw, status in [
             (dict(dt=3), DTYPE), (dict(dt=F32, hdt=BF16), UNSUPPORTED), (dict(C=20000), UNSUPPORTED), (dict(rows=-2), SHAPE),
