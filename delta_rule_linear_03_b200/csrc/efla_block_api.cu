@@ -164,7 +164,19 @@ efla_status_t check_conv(efla_dtype_t dtype, long long ldx, int B, int L, int C,
 // ---------------------------------------------------------------- scan
 
 // How the work is cut.  A block's recurrence is four warps, one a scheduler,
-// which alone leaves most of its latencies open: PLAN_COMMENT
+// which alone leaves most of its latencies open, so few blocks want short work
+// a token (two state values a lane) and many want little shared memory traffic
+// a value (two channels a lane).  us in the order of the kinds below:
+//   forward  1 x 4096 x 2048 x 16   91  157  278   segments 109 to 118
+//            2 x 4096 x 2048 x 16  165  173  337
+//            8 x 2048 x 1024 x 16  164  137  173
+//           16 x 1024 x 4096 x 16  564  457  444
+//            2 x 2048 x 1024 x 64  138  138  119
+//   backward 2 x 4096 x 2048 x 16  707  842
+//            8 x 2048 x 1024 x 16  676  550
+// Segments pay for a second pass over the exponentials, so they stand where
+// that fills idle SMs: 1 x 16384 x 512 x 16 396 -> 107 us, backward 2079 -> 344;
+// 1 x 4096 x 2048 x 16 backward 589 -> 380, where forward is better off whole.
 scan::Plan scan_plan(int B, int L, int C, int G, int N, bool bwd) {
     scan::Plan p;
     const int sms = num_sms(), cg = C / G;
@@ -419,8 +431,7 @@ efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_d
     a.B = B; a.L = L; a.C = C; a.run = conv_run(B, L, C); a.tiles = conv_tiles(L, a.run);
     a.dy = dy; a.dstate_out = dstate_out; a.dx = dx; a.dstate = dstate;
     const long long P = (long long)B * a.tiles;
-    a.part_w = static_cast<float *>(workspace);
-    a.part_b = a.part_w + P * C * K;
+    a.part = static_cast<float *>(workspace);
     const int row = a.head ? a.head : C;
     const bool vec = row % 2 == 0 && rows_in_vectors(x, ldx, 2, e);
     const dim3 grid((unsigned)P, (unsigned)((C + 32 * (vec ? 2 : 1) - 1) / (32 * (vec ? 2 : 1))));
@@ -433,8 +444,7 @@ efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_d
     }
     if (launched() != EFLA_OK) return EFLA_ERR_CUDA;
     const long long M = (long long)C * K;
-    if ((s = colsum(a.part_w, (int)P, ColsumOut{{dweight, nullptr, nullptr}, {M, M, M}}, M, st)) != EFLA_OK) return s;
-    return dbias ? colsum(a.part_b, (int)P, ColsumOut{{dbias, nullptr, nullptr}, {C, C, C}}, C, st) : EFLA_OK;
+    return colsum(a.part, (int)P, ColsumOut{{dweight, dbias, nullptr}, {M, M + C, M + C}}, M + C, st);
 }
 
 efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, void *state, const float *weight,

@@ -41,7 +41,7 @@ struct Args {
     // backward
     const void *dy, *dstate_out;
     void *dx, *dstate;
-    float *part_w, *part_b;  // [B * tiles][C * K], [B * tiles][C]
+    float *part;  // [B * tiles] rows of dw [C][K], dbias [C]
 };
 
 __device__ __forceinline__ int length_of(const Args &a, int b) {
@@ -355,14 +355,15 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
     for (int i = 0; i < VEC; ++i) mine[32 * VEC * K + lane * VEC + i] = f[i];
     __syncthreads();
     const int c0 = blockIdx.y * 32 * VEC, n = min(32 * VEC, a.C - c0);
+    float *part = a.part + (long long)blockIdx.x * a.C * (K + 1);
     for (int i = threadIdx.x; i < 32 * VEC * (K + 1); i += 32 * kWarps) {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) s += red[k][i];
         if (i < 32 * VEC * K) {
-            if (i < n * K) a.part_w[((long long)blockIdx.x * a.C + c0) * K + i] = s;
+            if (i < n * K) part[(long long)c0 * K + i] = s;
         } else if (i - 32 * VEC * K < n) {
-            a.part_b[(long long)blockIdx.x * a.C + c0 + i - 32 * VEC * K] = s;
+            part[(long long)a.C * K + c0 + i - 32 * VEC * K] = s;
         }
     }
 }
