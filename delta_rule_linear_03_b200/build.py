@@ -3,8 +3,10 @@
 Compiles ``csrc/efla_api.cu`` (the mixer), ``csrc/efla_block_api.cu`` (the
 operators around it) and ``csrc/efla_scan_*.cu`` (the scan's kernels), side by
 side for sm_100a only, and links them with the CUDA runtime, statically, so the
-library needs nothing but the driver at run time.  Rebuilds when any source under
-``csrc/`` or ``include/`` is newer than the library.
+library needs nothing but the driver at run time.  ``csrc/efla_block_binding.cpp``,
+the Python binding of the operators around the mixer, becomes
+``_efla_block.so``, against PyTorch's headers and the library.  Rebuilds when
+any source under ``csrc/`` or ``include/`` is newer than either.
 
     python delta_rule_linear_03_b200/build.py [--force]
 
@@ -21,8 +23,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libefla.so")
+BINDING = os.path.join(HERE, "_efla_block.so")
 SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu")) +
                  glob.glob(os.path.join(HERE, "csrc", "*.cuh")) +
+                 glob.glob(os.path.join(HERE, "csrc", "*.cpp")) +
                  glob.glob(os.path.join(ROOT, "include", "*.h")))
 UNITS = ("efla_api", "efla_block_api", "efla_scan_fwd_f32", "efla_scan_fwd_bf16", "efla_scan_bwd_f32", "efla_scan_bwd_bf16")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -37,10 +41,26 @@ def nvcc() -> str:
 
 
 def stale() -> bool:
-    if not os.path.exists(SO):
+    if not os.path.exists(SO) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(SO)
+    t = min(os.path.getmtime(SO), os.path.getmtime(BINDING))
     return any(os.path.getmtime(s) > t for s in SOURCES)
+
+
+def binding_command(out: str) -> list[str]:
+    """g++ on the binding's one source; the library is found beside it at run time."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_efla_block",
+            "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+            os.path.join(HERE, "csrc", "efla_block_binding.cpp"), "-o", out, "-L" + HERE, "-L" + lib, "-l:libefla.so",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -68,6 +88,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write("".join(said))
     os.replace(tmp, SO)
+    r = subprocess.run(binding_command(BINDING + f".tmp{os.getpid()}"), capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _efla_block.so")
+    os.replace(BINDING + f".tmp{os.getpid()}", BINDING)
     return SO
 
 

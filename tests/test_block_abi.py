@@ -191,10 +191,12 @@ def test_row_strides():
     """Tokens may lie apart evenly, a token's values may not."""
     import torch
 
-    from delta_rule_linear_03_b200.block import _rows
+    import delta_rule_linear_03_b200  # noqa: F401
+    from delta_rule_linear_03_b200 import _efla_block
 
     def ld(t, lead, tail):
-        return _rows(t, lead + tail, len(lead), t.dtype, -1, "t")  # -1: the host
+        assert tuple(t.shape) == lead + tail
+        return _efla_block.token_stride(t, len(lead))
 
     wide = torch.zeros(3, 5, 40)
     assert ld(wide, (3, 5), (40,)) == 40 and ld(wide[..., 8:24], (3, 5), (16,)) == 40
