@@ -12,6 +12,8 @@ using scan::rows_in_vectors;
 
 namespace {
 
+constexpr int kMaxLength = 0x7fff0000;  // of a sequence: tiles past its end still count in 32 bits
+
 // One buffer of a call: where it is, how many bytes from its first to its last.
 struct Buf {
     const void *p;
@@ -152,7 +154,7 @@ int conv_tiles(int L, int run) {
 
 efla_status_t check_conv(efla_dtype_t dtype, long long ldx, int B, int L, int C, int K, int heads) {
     if (!known_dtype(dtype)) return EFLA_ERR_DTYPE;
-    if (B < 0 || L < 0 || C < 0 || heads < 0 || K <= 0) return EFLA_ERR_SHAPE;
+    if (B < 0 || L < 0 || L > kMaxLength || C < 0 || heads < 0 || K <= 0) return EFLA_ERR_SHAPE;
     if (K < 2 || K > 4) return EFLA_ERR_UNSUPPORTED;
     if (heads && C % heads) return EFLA_ERR_SHAPE;
     if (ldx < C || ldx > kMaxElems) return EFLA_ERR_SHAPE;
@@ -240,7 +242,7 @@ BwdSizes bwd_sizes(const scan::Plan &p, int B, int L, int C, int G, int N) {
 
 efla_status_t check_scan(efla_dtype_t dtype, int B, int L, int C, int G, int N) {
     if (!known_dtype(dtype)) return EFLA_ERR_DTYPE;
-    if (B < 0 || L < 0 || C < 0 || G <= 0 || N <= 0) return EFLA_ERR_SHAPE;
+    if (B < 0 || L < 0 || L > kMaxLength || C < 0 || G <= 0 || N <= 0) return EFLA_ERR_SHAPE;
     if (N != 8 && N != 16 && N != 32 && N != 64) return EFLA_ERR_UNSUPPORTED;
     if (C % G) return EFLA_ERR_SHAPE;
     if ((double)B * (L + 1.0) * C > (double)kMaxElems || (double)B * (L + 1.0) * G * N > (double)kMaxElems ||
@@ -394,7 +396,7 @@ efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, co
 }
 
 size_t efla_conv_bwd_workspace_size(int B, int L, int C, int K) {
-    if (B <= 0 || L < 0 || C <= 0 || K < 2 || K > 4) return 0;
+    if (B <= 0 || L < 0 || L > kMaxLength || C <= 0 || K < 2 || K > 4) return 0;
     return round16((size_t)B * conv_tiles(L, conv_run(B, L, C)) * C * (K + 1) * sizeof(float));
 }
 

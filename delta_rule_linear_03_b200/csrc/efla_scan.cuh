@@ -263,6 +263,19 @@ template <typename S> __device__ __forceinline__ void scatter(float *p, int x, c
     }
 }
 
+// h exp(d A) + own: what a segment whose steps sum to d makes of the state (or
+// adjoint) that enters it.  By halves, for over many tokens the decay alone may
+// leave fp32's range where its product with h does not; a zero stays zero.
+template <int NP>
+__device__ __forceinline__ void pass_segment(f32x2 (&h)[NP], float d, const f32x2 (&A2)[NP], const f32x2 (&own)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        const float2 t = unpack2(ex2_2(mul2(twice(0.5f * d), A2[j])));
+        const f32x2 e = pack2(fminf(t.x, 3e38f), fminf(t.y, 3e38f));
+        h[j] = fma2(e, mul2(e, h[j]), own[j]);
+    }
+}
+
 // The state before the block's segment, composed of the segments before it.
 template <typename S>
 __device__ __forceinline__ void start_state(const Args &a, const Where &w, int c, int n0, int x,
@@ -276,8 +289,7 @@ __device__ __forceinline__ void start_state(const Args &a, const Where &w, int c
         const float d = a.seg_d[s * stride + bc];
         f32x2 own[S::NP];
         gather<S>(a.seg_h + (s * stride + bc) * S::N + n0, x, own);
-#pragma unroll
-        for (int j = 0; j < S::NP; ++j) h[j] = fma2(ex2_2(mul2(twice(d), A2[j])), h[j], own[j]);
+        pass_segment<S::NP>(h, d, A2, own);
     }
 }
 
@@ -658,8 +670,7 @@ __global__ void __launch_bounds__(2 * kThreads, S::N == 64 && S::CP == 2 ? 1 : 2
                 const float d = a.seg_d[s * stride + bc];
                 f32x2 own[NP];
                 gather<S>(a.seg_p + (s * stride + bc) * S::N + n0, ox, own);
-#pragma unroll
-                for (int j = 0; j < NP; ++j) p[i][j] = fma2(ex2_2(mul2(twice(d), A2[i][j])), p[i][j], own[j]);
+                pass_segment<NP>(p[i], d, A2[i], own);
             }
         }
         if (tiles)

@@ -187,6 +187,14 @@ def test_wrappers_refuse_host_tensors():
         efla.scan_fwd(x, x, torch.ones(8, 8), torch.ones(2, 4, 1, 8), torch.ones(2, 4, 1, 8))
 
 
+def test_lengths_that_tiles_cannot_count(so):
+    """A sequence so long that the tokens of its last tile pass 32 bits is refused."""
+    L = (1 << 31) - 1
+    assert conv_fwd(so, L=L, B=1) == SHAPE and conv_bwd(so, L=L, B=1) == SHAPE
+    assert scan_fwd(so, L=L, B=1) == SHAPE and scan_bwd(so, L=L, B=1) == SHAPE
+    assert so.efla_conv_bwd_workspace_size(1, L, 8, 4) == 0 == so.efla_scan_bwd_workspace_size(1, L, 8, 1, 8)
+
+
 def test_row_strides():
     """Tokens may lie apart evenly, a token's values may not."""
     import torch

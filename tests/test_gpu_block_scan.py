@@ -110,6 +110,25 @@ def test_scan_in_segments(efla, B, L, C, N, G, lengths, T):
     assert h2 is h and torch.equal(h, hl) and torch.equal(y2, y)
 
 
+def test_scan_segments_grow_and_decay_out_of_range(efla):
+    """A segment's whole decay may overflow or underflow where no state does."""
+    B, L, C, N = 1, 1000, 16, 16
+    assert efla.scan_fwd_workspace_size(B, L, C, 1, N) > 0
+    s = R.scan_inputs(B, L, C, N, 1, F)
+    s["A"] = torch.linspace(0.5, 1.0, C * N).reshape(C, N)  # growth of e^90 and more a segment, of a state of zeros
+    s["h0"] = torch.zeros(B, C, N)
+    s["x"][:, :690] = 0
+    s["dt"][:, :690], s["dt"][:, 690:], s["dt_bias"] = 1.0, -3.0, torch.zeros(C)
+    _check_fwd(efla, s)
+    # Decay of e^-96 in the first 160 tokens, from 10^30.  Each step is off by 2^-22 of itself at most and a sum of
+    # 160 of them by 160 2^-24, so the exponent by 96 (160 2^-24 + 2^-22) < 10^-3.
+    s["A"], s["h0"] = torch.full((C, N), -1.0), torch.full((B, C, N), 1e30)
+    s["x"][:], s["dt"][:, :160], s["dt"][:, 160:] = 0, -0.195, -300.0
+    _, h = _fwd(efla, s)
+    want = 1e30 * torch.exp(-160 * torch.nn.functional.softplus(s["dt"][0, 0, 0].double()))
+    assert 1e-20 < float(want) < 1e-10 and float((h.cpu().double() / want - 1).abs().max()) <= 1e-3
+
+
 def test_scan_padding_holds_anything(efla):
     s = R.scan_inputs(2, 70, 40, 16, 1, F, lengths=[33, 0])
     base = [t for t in _fwd(efla, s)] + [t for t in efla.scan_bwd(_cot(s)[0].cuda(), **_c(s))]
