@@ -60,7 +60,7 @@ def binding_command(out: str) -> list[str]:
             "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
             "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
             os.path.join(HERE, "csrc", "efla_block_binding.cpp"), "-o", out, "-L" + HERE, "-L" + lib, "-l:libefla.so",
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

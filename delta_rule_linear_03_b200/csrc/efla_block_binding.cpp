@@ -7,6 +7,7 @@
 // 13.  Each function returns the call's status first; block.py turns it into
 // an exception.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -103,8 +104,11 @@ void *out(const Opt &t) { return t ? t->mutable_data_ptr() : nullptr; }
 float *fout(const Tensor &t) { return t.mutable_data_ptr<float>(); }
 float *fout(const Opt &t) { return t ? t->mutable_data_ptr<float>() : nullptr; }
 
-Tensor fresh(const Tensor &like, IntArrayRef shape, at::ScalarType type) { return at::empty(shape, like.options().dtype(type)); }
-Tensor fresh(const Tensor &like, IntArrayRef shape) { return at::empty(shape, like.options()); }
+// Straight from the allocator: the dispatcher's way there takes as long again.
+Tensor fresh(const Tensor &like, IntArrayRef shape, at::ScalarType type) {
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
+Tensor fresh(const Tensor &like, IntArrayRef shape) { return fresh(like, shape, like.scalar_type()); }
 
 // A caller's output, checked, or a new one.
 Tensor output(const Opt &given, const Tensor &like, IntArrayRef shape, at::ScalarType type, int dev, const char *name) {
