@@ -54,8 +54,12 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
 // Threads of a row and vectors of a thread for nvec vectors: two vectors a
 // thread from 64 vectors on, so that the row's sums and root cost each
 // element less, and up to 512 threads (with 1024 a thread has 64 registers
-// and wide rows spill).
-#define EFLA_NORM_VEC(LAUNCH, T, nvec)                                     \
+// and wide rows spill).  From 513 to 1024 vectors, WIDE has four a thread, so
+// that several blocks stand on an SM and one's sums hide behind another's
+// loads (4096 x 8192, bf16 to bf16: 75 -> 64 us; backward, fp32, 8192 x 4096:
+// 95 -> 90); where registers do not allow that, the eight-bit output and the
+// bf16 backward pass, it loses (54 -> 74, 114 -> 177).
+#define EFLA_NORM_VEC(LAUNCH, T, nvec, WIDE)                                     \
     do {                                                                   \
         if ((nvec) <= 16) { LAUNCH(16, 1); }                               \
         else if ((nvec) <= 32) { LAUNCH(32, 1); }                          \
@@ -63,6 +67,7 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
         else if ((nvec) <= 128) { LAUNCH(64, 2); }                         \
         else if ((nvec) <= 256) { LAUNCH(128, 2); }                        \
         else if ((nvec) <= 512) { LAUNCH(256, 2); }                        \
+        else if ((nvec) <= 1024 && (WIDE)) { LAUNCH(256, 4); }             \
         else if ((nvec) <= 1024) { LAUNCH(512, 2); }                       \
         else if ((nvec) <= 2048) { LAUNCH(512, 4); }                       \
         else if constexpr (sizeof(T) == 4) { LAUNCH(512, 8); }             \
@@ -81,12 +86,22 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
 template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdArgs &a, bool vec, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     if (!vec) {
+        // vectors shifted to the row's alignment: up to VEC - 1 columns of the first and the last lie outside
+        const int shifted = (a.C + 2 * (VEC - 1)) / VEC;
 #define EFLA_L(WPR, IT)                                                                                        \
     norm::norm_fwd_any_kernel<T, R, WPR, IT>                                                                    \
         <<<(unsigned)((a.rows + norm::kThreadsOf<WPR * 32> / (WPR * 32) - 1) /                                   \
                       (norm::kThreadsOf<WPR * 32> / (WPR * 32))),                                                \
            norm::kThreadsOf<WPR * 32>, 0, st>>>(a)
-        EFLA_NORM_ANY(EFLA_L, a.C);
+#define EFLA_S(TPR, IT)                                                                                         \
+    if constexpr (TPR * IT * VEC > 128)                                                                         \
+    norm::norm_fwd_kernel<T, R, TPR, IT, 1, true><<<(unsigned)((a.rows + norm::kThreadsOf<TPR> / TPR - 1) /      \
+                                                               (norm::kThreadsOf<TPR> / TPR)),                  \
+                                                    norm::kThreadsOf<TPR>, 0, st>>>(a)
+        if (a.C <= 128) EFLA_L(1, 1);
+        else if (shifted > norm::kMaxC / VEC) EFLA_L(16, 8);
+        else EFLA_NORM_VEC(EFLA_S, T, shifted, !a.y8);
+#undef EFLA_S
 #undef EFLA_L
         return launched();
     }
@@ -96,13 +111,13 @@ template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdA
     do {                                                                                                    \
         constexpr int SL = norm::kThreadsOf<TPR> / TPR, RPI = IT == 1 ? 4 : IT == 2 ? 2 : 1;                \
         if (a.rows >= 2LL * num_sms() * SL * RPI)                                                           \
-            norm::norm_fwd_kernel<T, R, TPR, IT, RPI>                                                       \
+            norm::norm_fwd_kernel<T, R, TPR, IT, RPI, false>                                                       \
                 <<<(unsigned)((a.rows + SL * RPI - 1) / (SL * RPI)), norm::kThreadsOf<TPR>, 0, st>>>(a);     \
         else                                                                                                \
-            norm::norm_fwd_kernel<T, R, TPR, IT, 1>                                                         \
+            norm::norm_fwd_kernel<T, R, TPR, IT, 1, false>                                                         \
                 <<<(unsigned)((a.rows + SL - 1) / SL), norm::kThreadsOf<TPR>, 0, st>>>(a);                   \
     } while (0)
-    EFLA_NORM_VEC(EFLA_L, T, nvec);
+    EFLA_NORM_VEC(EFLA_L, T, nvec, !a.y8);
 #undef EFLA_L
     return launched();
 }
@@ -122,7 +137,7 @@ template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdA
     const int nvec = a.C / VEC;
 #define EFLA_L(TPR, IT) \
     norm::norm_bwd_kernel<T, R, TPR, IT, (IT == 1 || (IT == 2 && sizeof(T) == 4) ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
-    EFLA_NORM_VEC(EFLA_L, T, nvec);
+    EFLA_NORM_VEC(EFLA_L, T, nvec, sizeof(T) == 4);
 #undef EFLA_L
     return launched();
 }

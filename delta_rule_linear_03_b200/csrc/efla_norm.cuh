@@ -127,8 +127,40 @@ struct FwdArgs {
     long long rows;
 };
 
-// Rows whose width is a multiple of the 16-byte vector.
-template <typename T, typename R, int TPR, int IT, int RPI>
+// VEC columns from c on; ANY: those of them that are columns of the row, each
+// vector aligned although the row is not.
+template <bool ANY, typename T, int VEC> __device__ __forceinline__ Raw<T, VEC> load_cols(const T *row, int c, int C, bool on) {
+    if constexpr (ANY) {
+        Raw<T, VEC> r = zero_raw<T, VEC>();
+        if (on && c >= 0 && c + VEC <= C) return load_raw<T, VEC>(row + c);
+        if (on && c < C)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (c + j >= 0 && c + j < C) r.e[j] = row[c + j];
+        return r;
+    } else {
+        return on && c < C ? load_raw<T, VEC>(row + c) : zero_raw<T, VEC>();
+    }
+}
+template <bool ANY, typename T, int VEC>
+__device__ __forceinline__ void store_cols(T *row, int c, int C, bool on, const Raw<T, VEC> &r) {
+    if (!on || c >= C) return;
+    if (!ANY || (c >= 0 && c + VEC <= C)) {
+        store_raw<T, VEC>(row + c, r);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j >= 0 && c + j < C) row[c + j] = r.e[j];
+    }
+}
+
+// Rows in 16-byte vectors.  ANY: the width is no multiple of them, so a row's
+// vectors begin at the 16-byte boundary before it, and one vector of a group of
+// 128 columns begins in the group before; the groups' maxima meet in shared
+// memory.  Element by element instead, as norm_fwd_any_kernel has it, 33520 x
+// 1001 took 259 us in fp32 (83 with vectors) and 166 in bf16 (108); up to 128
+// columns, with two cut vectors in every few, it is the faster (74 against 159).
+template <typename T, typename R, int TPR, int IT, int RPI, bool ANY>
 __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
     constexpr int VEC = 16 / sizeof(T), SLOTS = kThreadsOf<TPR> / TPR;
     constexpr int LPG = kGroup / VEC < TPR ? kGroup / VEC : TPR;  // lanes of one group of 128 columns
@@ -137,6 +169,15 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
     const long long row0 = (long long)blockIdx.x * (SLOTS * RPI) + slot;
     const T *x = static_cast<const T *>(a.x);
     const R *res = static_cast<const R *>(a.res);
+    const int off = ANY ? (int)(row0 * C & (VEC - 1)) : 0;
+    static_assert(!ANY || RPI == 1, "one row, one offset");
+    constexpr int NG = ANY ? TPR * IT * VEC / kGroup + 2 : 1;
+    __shared__ int gmax[ANY ? SLOTS : 1][NG];  // maxima as bits, whose order is the values'; a NaN is the largest
+    if (ANY) {
+        for (int g = threadIdx.x; g < SLOTS * NG; g += kThreadsOf<TPR>) (&gmax[0][0])[g] = 0;
+        __syncthreads();
+    }
+    const auto col = [&](int k) { return (k * TPR + l) * VEC - off; };
 
     Raw<T, VEC> xr[RPI][IT];
     Raw<R, VEC> rr[RPI][IT];
@@ -145,10 +186,8 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const long long row = row0 + i * SLOTS;
-            const int c = (k * TPR + l) * VEC;
-            const bool in = row < a.rows && c < C;
-            xr[i][k] = in ? load_raw<T, VEC>(x + row * C + c) : zero_raw<T, VEC>();
-            if (res) rr[i][k] = in ? load_raw<R, VEC>(res + row * C + c) : zero_raw<R, VEC>();
+            xr[i][k] = load_cols<ANY, T, VEC>(x + row * C, col(k), C, row < a.rows);
+            if (res) rr[i][k] = load_cols<ANY, R, VEC>(res + row * C, col(k), C, row < a.rows);
         }
     f32x2 h[RPI][IT][VEC / 2];
     float ss[RPI];
@@ -172,8 +211,15 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
     f32x2 w[IT][VEC / 2];
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-        const int c = (k * TPR + l) * VEC;
-        widen2<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
+        const int c = col(k);
+        if constexpr (ANY) {
+            Raw<float, VEC> r;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) r.e[j] = a.w[min(max(c + j, 0), C - 1)];
+            widen2<float, VEC>(r, w[k]);
+        } else {
+            widen2<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
+        }
     }
     rs.sum(ss);
     // columns past C hold zeros, which are no part of a maximum (their product with an infinite
@@ -186,13 +232,13 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
         top[i] = 0.f;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int c = (k * TPR + l) * VEC;
+            const int c = col(k);
             const bool in = row < a.rows && c < C;
-            if (a.res_out && in) store_raw<R, VEC>(static_cast<R *>(a.res_out) + row * C + c, narrow2<R, VEC>(h[i][k]));
+            if (a.res_out) store_cols<ANY, R, VEC>(static_cast<R *>(a.res_out) + row * C, c, C, in, narrow2<R, VEC>(h[i][k]));
             const f32x2 r2 = in ? pack2(rstd, rstd) : 0ull;
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) h[i][k][j] = mul2(mul2(h[i][k][j], r2), w[k][j]);
-            if (a.y && in) store_raw<T, VEC>(static_cast<T *>(a.y) + row * C + c, narrow2<T, VEC>(h[i][k]));
+            if (a.y) store_cols<ANY, T, VEC>(static_cast<T *>(a.y) + row * C, c, C, in, narrow2<T, VEC>(h[i][k]));
         }
     }
     if (!a.y8) return;
@@ -209,14 +255,35 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
         rm.max_abs(top);
     }
     const int ng = a.group ? (C + kGroup - 1) / kGroup : 1;
+    if (ANY && a.group) {
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+            const int v0 = col(k) + off, g = v0 / kGroup, cut = v0 % kGroup ? 0 : off;  // columns before `cut` are group g - 1's
+            float lo = 0.f, hi = 0.f;
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                const float2 t = unpack2(h[0][k][j]);
+                if (2 * j < cut) lo = max_abs(lo, t.x); else hi = max_abs(hi, t.x);
+                if (2 * j + 1 < cut) lo = max_abs(lo, t.y); else hi = max_abs(hi, t.y);
+            }
+#pragma unroll
+            for (int o = LPG / 2; o > 0; o >>= 1) hi = max_abs(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            if (l % LPG == 0) atomicMax(&gmax[slot][g], __float_as_int(hi));
+            if (cut && g > 0) atomicMax(&gmax[slot][g - 1], __float_as_int(lo));
+        }
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < RPI; ++i) {
         const long long row = row0 + i * SLOTS;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int c = (k * TPR + l) * VEC;
+            const int c = col(k);
             float m = top[i];
-            if (a.group) {
+            const int g = (c + off) / kGroup, cut = ANY && a.group && (c + off) % kGroup == 0 ? off : 0;
+            if (ANY && a.group) {
+                m = __int_as_float(gmax[slot][g]);
+            } else if (a.group) {
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) {
                     const float2 t = unpack2(h[i][k][j]);
@@ -227,14 +294,23 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
             }
             const float s = scale_of(m), inv = rcp(s);
             if (row >= a.rows || c >= C) continue;
-            if (a.group ? l % LPG == 0 : (l == 0 && k == 0)) a.scale[row * ng + (a.group ? c / kGroup : 0)] = s;
+            if (a.group ? l % LPG == 0 && g < ng : l == 0 && k == 0) a.scale[row * ng + (a.group ? g : 0)] = s;
+            const float low = cut && g > 0 ? rcp(scale_of(__int_as_float(gmax[slot][g - 1]))) : inv;
             uint16_t q[VEC / 2];
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) {
-                const float2 t = unpack2(mul2(h[i][k][j], pack2(inv, inv)));
+                const float2 t = unpack2(mul2(h[i][k][j], ANY ? pack2(2 * j < cut ? low : inv, 2 * j + 1 < cut ? low : inv) : pack2(inv, inv)));
                 q[j] = e4m3x2(t.x, t.y);
             }
             unsigned char *p = a.y8 + row * C + c;
+            if constexpr (ANY) {
+                if (c < 0 || c + VEC > C) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        if (c + j >= 0 && c + j < C) p[j] = (unsigned char)(q[j / 2] >> (j % 2 * 8));
+                    continue;
+                }
+            }
             if constexpr (VEC == 8)
                 *reinterpret_cast<uint2 *>(p) =
                     make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
@@ -244,7 +320,8 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
     }
 }
 
-// Any width: WPR warps share a row, each takes whole groups of 128 columns,
+// Few columns, or a width that the vectors of norm_fwd_kernel do not reach:
+// WPR warps share a row, each takes whole groups of 128 columns,
 // IT of them, four single elements a lane, so that a group's maximum stays
 // within one warp.
 template <typename T, typename R, int WPR, int IT>

@@ -65,6 +65,16 @@ def test_norm_fwd_eight_bits(efla, rows, C, T, RT, group):
         R.close(out, rh, rh.abs(), 1, "res_out")
 
 
+@pytest.mark.parametrize("rows,C", [(9, 130), (70, 255), (9, 385), (9, 511), (9, 514), (9, 1029), (700, 1001), (9, 2047), (9, 4099), (9, 6145), (9, 12289),
+                                    (9, 16369), (9, 16371)])
+@pytest.mark.parametrize("T,RT", [(BF, None), (BF, F), (F, F)])
+def test_norm_fwd_rows_off_their_boundary(efla, rows, C, T, RT):
+    """Rows that begin at every offset from a 16-byte boundary."""
+    test_norm_fwd(efla, rows, C, T, RT)
+    for group in (0, 128):
+        test_norm_fwd_eight_bits(efla, rows, C, T, RT, group)
+
+
 @pytest.mark.parametrize("rows,C", SIZES)
 @pytest.mark.parametrize("T,HT,dres", [(BF, BF, True), (BF, BF, False), (BF, F, True), (BF, F, False), (F, F, True), (F, F, False)])
 def test_norm_bwd(efla, rows, C, T, HT, dres):
@@ -95,7 +105,7 @@ def test_norm_leading_dimensions(efla):
     assert y.shape == (2, 3, 5, 64) and scale.shape == (2, 3, 5, 1)
 
 
-@pytest.mark.parametrize("C", [100, 1024, 4096])
+@pytest.mark.parametrize("C", [100, 1001, 1024, 4096])
 def test_norm_in_place(efla, C):
     x, wt, res = _draw(50, C, BF, BF)
     y, _, out = efla.norm_fwd(x.cuda(), wt.cuda(), res.cuda())
