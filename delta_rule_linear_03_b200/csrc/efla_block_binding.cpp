@@ -197,8 +197,8 @@ std::tuple<int, Tensor, Tensor, Tensor> norm_bwd(const Tensor &dy, const Tensor 
     want(dres_out, shape, HT, dev, "dres_out");
     want(weight, {C}, at::kFloat, dev, "weight");
     const Tensor dx = fresh(dy, shape), dres = HT == T ? dx : fresh(h, shape), dw = fresh(dy, {C}, at::kFloat);
-    const Scratch ws(efla_norm_bwd_workspace_size(rows, C), workspace, dy);
     const Call call(dev);
+    const Scratch ws(efla_norm_bwd_workspace_size(rows, C), workspace, dy);
     const int s = efla_norm_bwd(ptr(dy), code(T), ptr(h), code(HT), f32(weight), (float)eps, ptr(dres_out), out(dx),
                                 HT == T ? nullptr : out(dres), fout(dw), rows, C, ws.p, ws.n, call.stream);
     return {s, dx, dres, dw};
@@ -249,8 +249,8 @@ std::tuple<int, Tensor, Tensor, Opt, Opt> conv_bwd(const Tensor &dy, const Tenso
     Opt db, ds;
     if (bias) db = fresh(x, {c.C}, at::kFloat);
     if (state) ds = fresh(x, {c.B, c.K - 1, c.C});
-    const Scratch ws(efla_conv_bwd_workspace_size(c.B, c.L, c.C, c.K), workspace, x);
     const Call call(c.dev);
+    const Scratch ws(efla_conv_bwd_workspace_size(c.B, c.L, c.C, c.K), workspace, x);
     const int s = efla_conv_bwd(ptr(dy), ptr(x), c.ldx, code(c.T), f32(weight), f32(bias), ptr(state), i32(lengths), silu,
                                 (int)heads, ptr(dstate_out), out(dx), fout(dw), fout(db), out(ds), c.B, c.L, c.C, c.K, ws.p,
                                 ws.n, call.stream);
@@ -314,8 +314,8 @@ std::tuple<int, Tensor, Opt> scan_fwd(const Tensor &x, const Tensor &dt, const T
     const Tensor y = output(y_, x, c.shape, c.T, c.dev, "y");
     Opt hL;
     if (h_L_ || want_state) hL = output(h_L_, x, {c.B, c.C, c.N}, at::kFloat, c.dev, "h_L");
-    const Scratch ws(efla_scan_fwd_workspace_size(c.B, c.L, c.C, c.G, c.N), workspace, x);
     const Call call(c.dev);
+    const Scratch ws(efla_scan_fwd_workspace_size(c.B, c.L, c.C, c.G, c.N), workspace, x);
     const int s = efla_scan_fwd(ptr(x), c.ldx, ptr(dt), c.lddt, f32(A), ptr(Bm), c.ldb, ptr(Cm), c.ldc, f32(D), ptr(z), c.ldz,
                                 f32(bias), f32(h0), i32(lengths), code(c.T), softplus, out(y), fout(hL), c.B, c.L, c.C, c.G,
                                 c.N, ws.p, ws.n, call.stream);
@@ -336,8 +336,8 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor, Tensor, Opt, Opt, Opt, Tensor> s
     if (D) dD = fresh(x, {c.C}, at::kFloat);
     if (z) dz = fresh(x, c.shape);
     if (bias) db = fresh(x, {c.C}, at::kFloat);
-    const Scratch ws(efla_scan_bwd_workspace_size(c.B, c.L, c.C, c.G, c.N), workspace, x);
     const Call call(c.dev);
+    const Scratch ws(efla_scan_bwd_workspace_size(c.B, c.L, c.C, c.G, c.N), workspace, x);
     const int s = efla_scan_bwd(ptr(dy), ptr(x), c.ldx, ptr(dt), c.lddt, f32(A), ptr(Bm), c.ldb, ptr(Cm), c.ldc, f32(D), ptr(z),
                                 c.ldz, f32(bias), f32(h0), i32(lengths), f32(dh_L), code(c.T), softplus, out(dx), out(ddt),
                                 fout(dA), out(dB), out(dC), fout(dD), out(dz), fout(db), fout(dh0), c.B, c.L, c.C, c.G, c.N,

@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) norm_bwd_
         for (int i = 0; i < RPI; ++i) {
             const long long row = base + i * SLOTS + slot;
             const float rstd = rstd_of(fmaf(s[2 * i], a.inv_c, a.eps));
-            const float m = rstd * rstd * (s[2 * i + 1] * a.inv_c);
+            const float m = rstd * (rstd * (s[2 * i + 1] * a.inv_c));  // the square alone may overflow
 #pragma unroll
             for (int k = 0; k < IT; ++k) {
                 const int c = (k * TPR + l) * VEC;
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreadsOf<WPR * 32>, WPR <= 8 ? 2 : 1) norm_b
             }
         rs[par].sum(s);
         const float rstd = rstd_of(fmaf(s[0], a.inv_c, a.eps));
-        const float m = rstd * rstd * (s[1] * a.inv_c);
+        const float m = rstd * (rstd * (s[1] * a.inv_c));
 #pragma unroll
         for (int k = 0; k < IT; ++k)
 #pragma unroll
