@@ -51,15 +51,58 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
 
 // ---------------------------------------------------------------- norm
 
+// Rows of up to 64 vectors share blocks of 256 threads; longer ones have a
+// block of their own, of the whole warps that they need: with powers of two
+// 16384 x 2048 in bf16 to 8 bits took 40.3 us (39.0 so), 21845 x 1536 46 (39),
+// 6553 x 5120 75 (46).
+template <typename T, typename R, int TPR, int IT, int RPI, bool ANY>
+efla_status_t launch_norm_rows(const norm::FwdArgs &a, int nvec, cudaStream_t st) {
+    const int threads = TPR > 0 ? norm::kThreadsOf<TPR> : (nvec + 32 * IT - 1) / (32 * IT) * 32;
+    const long long rows = (long long)RPI * (TPR > 0 ? threads / TPR : 1);  // of a block
+    // several rows in flight a thread once there are enough to fill the SMs
+    if constexpr (RPI > 1)
+        if (a.rows * threads < 512LL * num_sms() * rows) return launch_norm_rows<T, R, TPR, IT, 1, ANY>(a, nvec, st);
+    norm::norm_fwd_kernel<T, R, TPR, IT, RPI, ANY><<<(unsigned)((a.rows + rows - 1) / rows), threads, 0, st>>>(a);
+    return launched();
+}
+
+template <typename T, typename R, bool ANY> efla_status_t launch_norm_vectors(const norm::FwdArgs &a, int nvec, cudaStream_t st) {
+    constexpr int R4 = ANY ? 1 : 4, R2 = ANY ? 1 : 2;
+    if constexpr (!ANY) {
+        if (nvec <= 16) return launch_norm_rows<T, R, 16, 1, R4, ANY>(a, nvec, st);
+        if (nvec <= 32) return launch_norm_rows<T, R, 32, 1, R4, ANY>(a, nvec, st);
+    }
+    if (nvec <= 64) return launch_norm_rows<T, R, 32, 2, R2, ANY>(a, nvec, st);
+    // two vectors a thread; four from 513 vectors on, for more blocks an SM (4096 x 8192, bf16 to bf16: 75 -> 72 us,
+    // 6553 x 5120: 74 -> 66), but where the eight-bit output needs the registers (4096 x 8192: 54 -> 74)
+    if (nvec <= (a.y8 ? 1024 : 512)) return launch_norm_rows<T, R, -512, 2, R2, ANY>(a, nvec, st);
+    if (nvec <= 2048) return launch_norm_rows<T, R, -512, 4, 1, ANY>(a, nvec, st);
+    if constexpr (sizeof(T) == 4) return launch_norm_rows<T, R, -512, 8, 1, ANY>(a, nvec, st);
+    return EFLA_ERR_UNSUPPORTED;
+}
+
+template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdArgs &a, bool vec, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    if (vec) return launch_norm_vectors<T, R, false>(a, a.C / VEC, st);
+    // vectors shifted to the row's alignment: up to VEC - 1 columns of the first and the last lie outside
+    const int shifted = (a.C + 2 * (VEC - 1)) / VEC;
+    if (a.C > 128 && shifted <= norm::kMaxC / VEC) return launch_norm_vectors<T, R, true>(a, shifted, st);
+    if (a.C <= 128) norm::norm_fwd_any_kernel<T, R, 1, 1><<<(unsigned)((a.rows + 7) / 8), 256, 0, st>>>(a);
+    else norm::norm_fwd_any_kernel<T, R, 16, 8><<<(unsigned)a.rows, 512, 0, st>>>(a);
+    return launched();
+}
+
+// Blocks of the backward pass, each with a row of partial column sums: as
+// many as are resident at once, fewer where there are fewer rows.
+long long norm_bwd_blocks(long long rows) { return std::min<long long>(rows, 2LL * num_sms()); }
+
 // Threads of a row and vectors of a thread for nvec vectors: two vectors a
 // thread from 64 vectors on, so that the row's sums and root cost each
 // element less, and up to 512 threads (with 1024 a thread has 64 registers
-// and wide rows spill).  From 513 to 1024 vectors, WIDE has four a thread, so
-// that several blocks stand on an SM and one's sums hide behind another's
-// loads (4096 x 8192, bf16 to bf16: 75 -> 64 us; backward, fp32, 8192 x 4096:
-// 95 -> 90); where registers do not allow that, the eight-bit output and the
-// bf16 backward pass, it loses (54 -> 74, 114 -> 177).
-#define EFLA_NORM_VEC(LAUNCH, T, nvec, WIDE)                                     \
+// and wide rows spill).  In fp32, rows of 513 to 1024 vectors have four a
+// thread, and two blocks an SM (8192 x 4096: 95 -> 90 us); in bf16 that
+// spills (4096 x 8192: 114 -> 177).
+#define EFLA_NORM_VEC(LAUNCH, T, nvec)                                     \
     do {                                                                   \
         if ((nvec) <= 16) { LAUNCH(16, 1); }                               \
         else if ((nvec) <= 32) { LAUNCH(32, 1); }                          \
@@ -67,8 +110,7 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
         else if ((nvec) <= 128) { LAUNCH(64, 2); }                         \
         else if ((nvec) <= 256) { LAUNCH(128, 2); }                        \
         else if ((nvec) <= 512) { LAUNCH(256, 2); }                        \
-        else if ((nvec) <= 1024 && (WIDE)) { LAUNCH(256, 4); }             \
-        else if ((nvec) <= 1024) { LAUNCH(512, 2); }                       \
+        else if ((nvec) <= 1024) { LAUNCH((sizeof(T) == 4 ? 256 : 512), (sizeof(T) == 4 ? 4 : 2)); } \
         else if ((nvec) <= 2048) { LAUNCH(512, 4); }                       \
         else if constexpr (sizeof(T) == 4) { LAUNCH(512, 8); }             \
     } while (0)
@@ -83,49 +125,6 @@ efla_status_t colsum(const float *part, int P, ColsumOut o, long long M, cudaStr
         else { LAUNCH(16, 8); }                          \
     } while (0)
 
-template <typename T, typename R> efla_status_t launch_norm_fwd(const norm::FwdArgs &a, bool vec, cudaStream_t st) {
-    constexpr int VEC = 16 / sizeof(T);
-    if (!vec) {
-        // vectors shifted to the row's alignment: up to VEC - 1 columns of the first and the last lie outside
-        const int shifted = (a.C + 2 * (VEC - 1)) / VEC;
-#define EFLA_L(WPR, IT)                                                                                        \
-    norm::norm_fwd_any_kernel<T, R, WPR, IT>                                                                    \
-        <<<(unsigned)((a.rows + norm::kThreadsOf<WPR * 32> / (WPR * 32) - 1) /                                   \
-                      (norm::kThreadsOf<WPR * 32> / (WPR * 32))),                                                \
-           norm::kThreadsOf<WPR * 32>, 0, st>>>(a)
-#define EFLA_S(TPR, IT)                                                                                         \
-    if constexpr (TPR * IT * VEC > 128)                                                                         \
-    norm::norm_fwd_kernel<T, R, TPR, IT, 1, true><<<(unsigned)((a.rows + norm::kThreadsOf<TPR> / TPR - 1) /      \
-                                                               (norm::kThreadsOf<TPR> / TPR)),                  \
-                                                    norm::kThreadsOf<TPR>, 0, st>>>(a)
-        if (a.C <= 128) EFLA_L(1, 1);
-        else if (shifted > norm::kMaxC / VEC) EFLA_L(16, 8);
-        else EFLA_NORM_VEC(EFLA_S, T, shifted, !a.y8);
-#undef EFLA_S
-#undef EFLA_L
-        return launched();
-    }
-    const int nvec = a.C / VEC;
-    // four rows in flight a thread once there are rows enough for two blocks an SM
-#define EFLA_L(TPR, IT)                                                                                     \
-    do {                                                                                                    \
-        constexpr int SL = norm::kThreadsOf<TPR> / TPR, RPI = IT == 1 ? 4 : IT == 2 ? 2 : 1;                \
-        if (a.rows >= 2LL * num_sms() * SL * RPI)                                                           \
-            norm::norm_fwd_kernel<T, R, TPR, IT, RPI, false>                                                       \
-                <<<(unsigned)((a.rows + SL * RPI - 1) / (SL * RPI)), norm::kThreadsOf<TPR>, 0, st>>>(a);     \
-        else                                                                                                \
-            norm::norm_fwd_kernel<T, R, TPR, IT, 1, false>                                                         \
-                <<<(unsigned)((a.rows + SL - 1) / SL), norm::kThreadsOf<TPR>, 0, st>>>(a);                   \
-    } while (0)
-    EFLA_NORM_VEC(EFLA_L, T, nvec, !a.y8);
-#undef EFLA_L
-    return launched();
-}
-
-// Blocks of the backward pass, each with a row of partial column sums: as
-// many as are resident at once, fewer where there are fewer rows.
-long long norm_bwd_blocks(long long rows) { return std::min<long long>(rows, 2LL * num_sms()); }
-
 template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdArgs &a, bool vec, int blocks, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     if (!vec) {
@@ -137,7 +136,7 @@ template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdA
     const int nvec = a.C / VEC;
 #define EFLA_L(TPR, IT) \
     norm::norm_bwd_kernel<T, R, TPR, IT, (IT == 1 || (IT == 2 && sizeof(T) == 4) ? 2 : 1)><<<blocks, norm::kThreadsOf<TPR>, 0, st>>>(a)
-    EFLA_NORM_VEC(EFLA_L, T, nvec, sizeof(T) == 4);
+    EFLA_NORM_VEC(EFLA_L, T, nvec);
 #undef EFLA_L
     return launched();
 }

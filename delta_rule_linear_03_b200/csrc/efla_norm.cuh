@@ -9,16 +9,16 @@
 //
 // HBM bound: a handful of flops an element.  A row stays in registers
 // between the sum of its squares and its output, so each tensor crosses HBM
-// once.  TPR threads share a row with 16-byte accesses, IT of them each, and
-// RPI rows are in flight a thread; the row's sums go through shuffles and,
-// from 64 threads on, one exchange in shared memory for all RPI rows.  h is
+// once.  TPR threads, or a block, share a row with 16-byte accesses, IT of them
+// each, and RPI rows are in flight a thread; the row's sums go through shuffles
+// and, past a warp, one exchange in shared memory for all RPI rows.  h is
 // the unrounded fp32 sum for the norm; res_out is its rounding.
 //
 // Measured, of a copy's 6.57 TB/s: 65536 x 2048, bf16 with residual to 8 bits
-// 142 us (all of it; element by element in fp32 it took 272, bound by the ALUs,
+// 137 us (all of it; element by element in fp32 it took 272, bound by the ALUs,
 // which now stand at 62%, hence paired operations and conversions); 131008
-// x 128, fp32, 22.3 us (92%); 16384 x 2048 backward, bf16 with an fp32
-// residual, 90.6 us (90%).  64 rows are a launch: 2.3 us.
+// x 128, fp32, 22.4 us (91%); 16384 x 2048 backward, bf16 with an fp32
+// residual, 90.6 us (90%).  64 rows are a launch: 2.4 us.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -32,7 +32,9 @@ constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: no scale is 0 or subnor
 constexpr int kGroup = 128;
 constexpr int kMaxC = 16384;
 
-template <int TPR> constexpr int kThreadsOf = TPR > 256 ? TPR : 256;
+// Threads of a block whose rows have TPR threads each; TPR < 0: the block is
+// the row's, as large as the row needs, up to -TPR threads.
+template <int TPR> constexpr int kThreadsOf = TPR < 0 ? -TPR : TPR > 256 ? TPR : 256;
 
 // The larger magnitude; a NaN stays one.
 __device__ __forceinline__ float max_abs(float a, float b) {
@@ -43,48 +45,48 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 
 // Sums or maxima of V values over the TPR threads of a row.
 template <int TPR, int V> struct RowReduce {
-    static constexpr int NW = kThreadsOf<TPR> / 32;
-    float red[TPR > 32 ? V : 1][TPR > 32 ? NW : 1];
+    static constexpr bool kWarps = TPR < 0 || TPR > 32;  // a row has several
+    static constexpr int NW = kThreadsOf<TPR> / 32, LANES = kWarps ? 32 : TPR;
+    float red[kWarps ? V : 1][kWarps ? NW : 1];
 
-    __device__ __forceinline__ void sum(float (&v)[V]) {
+    template <typename F> __device__ __forceinline__ void reduce(float (&v)[V], F f) {
 #pragma unroll
-        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+        for (int o = LANES / 2; o > 0; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        if constexpr (TPR > 32) {
-            const int warp = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0)
+            for (int i = 0; i < V; ++i) v[i] = f(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+        if constexpr (kWarps) {
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            if (lane == 0)
 #pragma unroll
                 for (int i = 0; i < V; ++i) red[i][warp] = v[i];
             __syncthreads();
-            const int w0 = warp / (TPR / 32) * (TPR / 32);
+            if constexpr (TPR < 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float s = 0.f;
+                for (int i = 0; i < V; ++i) v[i] = lane < blockDim.x / 32 ? red[i][lane] : 0.f;  // no more than NW
 #pragma unroll
-                for (int k = 0; k < TPR / 32; ++k) s += red[i][w0 + k];
-                v[i] = s;
+                for (int o = NW / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = f(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+            } else {
+                const int w0 = warp / (TPR / 32) * (TPR / 32);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float s = red[i][w0];
+#pragma unroll
+                    for (int k = 1; k < TPR / 32; ++k) s = f(s, red[i][w0 + k]);
+                    v[i] = s;
+                }
             }
         }
     }
+    __device__ __forceinline__ void sum(float (&v)[V]) {
+        reduce(v, [](float a, float b) { return a + b; });
+    }
     // largest of values that are magnitudes; a NaN stays one
     __device__ __forceinline__ void max_abs(float (&v)[V]) {
-#pragma unroll
-        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = norm::max_abs(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
-        if constexpr (TPR > 32) {
-            const int warp = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int i = 0; i < V; ++i) red[i][warp] = v[i];
-            __syncthreads();
-            const int w0 = warp / (TPR / 32) * (TPR / 32);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int k = 0; k < TPR / 32; ++k) v[i] = norm::max_abs(v[i], red[i][w0 + k]);
-        }
+        reduce(v, [](float a, float b) { return norm::max_abs(a, b); });
     }
 };
 
@@ -164,26 +166,27 @@ __device__ __forceinline__ void store_cols(T *row, int c, int C, bool on, const 
 // vectors begin at the 16-byte boundary before it, and one vector of a group of
 // 128 columns begins in the group before; the groups' maxima meet in shared
 // memory.  Element by element instead, as norm_fwd_any_kernel has it, 33520 x
-// 1001 took 259 us in fp32 (83 with vectors) and 166 in bf16 (108); up to 128
+// 1001 took 259 us in fp32 (82 with vectors) and 166 in bf16 (95); up to 128
 // columns, with two cut vectors in every few, it is the faster (74 against 159).
 template <typename T, typename R, int TPR, int IT, int RPI, bool ANY>
 __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
-    constexpr int VEC = 16 / sizeof(T), SLOTS = kThreadsOf<TPR> / TPR;
-    constexpr int LPG = kGroup / VEC < TPR ? kGroup / VEC : TPR;  // lanes of one group of 128 columns
+    constexpr int VEC = 16 / sizeof(T), SLOTS = TPR > 0 ? kThreadsOf<TPR> / TPR : 1;
+    constexpr int LPG = TPR > 0 && kGroup / VEC > TPR ? TPR : kGroup / VEC;  // lanes of one group of 128 columns
+    const int tpr = TPR > 0 ? TPR : blockDim.x;
     __shared__ RowReduce<TPR, RPI> rs, rm;
-    const int slot = threadIdx.x / TPR, l = threadIdx.x % TPR, C = a.C;
+    const int slot = TPR > 0 ? threadIdx.x / tpr : 0, l = TPR > 0 ? threadIdx.x % tpr : threadIdx.x, C = a.C;
     const long long row0 = (long long)blockIdx.x * (SLOTS * RPI) + slot;
     const T *x = static_cast<const T *>(a.x);
     const R *res = static_cast<const R *>(a.res);
     const int off = ANY ? (int)(row0 * C & (VEC - 1)) : 0;
     static_assert(!ANY || RPI == 1, "one row, one offset");
-    constexpr int NG = ANY ? TPR * IT * VEC / kGroup + 2 : 1;
+    constexpr int NG = ANY ? (TPR > 0 ? TPR : -TPR) * IT * VEC / kGroup + 2 : 1;
     __shared__ int gmax[ANY ? SLOTS : 1][NG];  // maxima as bits, whose order is the values'; a NaN is the largest
     if (ANY) {
-        for (int g = threadIdx.x; g < SLOTS * NG; g += kThreadsOf<TPR>) (&gmax[0][0])[g] = 0;
+        for (int g = threadIdx.x; g < SLOTS * NG; g += blockDim.x) (&gmax[0][0])[g] = 0;
         __syncthreads();
     }
-    const auto col = [&](int k) { return (k * TPR + l) * VEC - off; };
+    const auto col = [&](int k) { return (k * tpr + l) * VEC - off; };
 
     Raw<T, VEC> xr[RPI][IT];
     Raw<R, VEC> rr[RPI][IT];
