@@ -1,6 +1,8 @@
 // efla_block_api.cu - the C ABI of the operators around the mixer (norm,
 // short convolution, selective scan): validation, scratch sizing and kernel
 // dispatch, as efla_api.cu has them for the mixer itself.
+#include <cmath>
+
 #include "efla_conv.cuh"
 #include "efla_host.cuh"
 #include "efla_norm.cuh"
@@ -150,20 +152,35 @@ template <typename T, typename R> efla_status_t launch_norm_bwd(const norm::BwdA
         else KERNEL<T, 4, VEC><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                                \
     } while (0)
 
+int conv_tiles(int L, int run) {
+    const int n = run * conv::kWarps;
+    return L > 0 ? (L + n - 1) / n : 1;
+}
+
 // Tokens of a thread's run: long ones read fewer rows twice and load their
-// filters less often (4 x 4096 x 2048, bf16: 30.0 us forward and 64 backward
-// with 128 tokens, 32.5 and 73 with 64), short ones give a short or narrow
-// input enough threads, four blocks an SM.
+// filters less often, short ones give a short or narrow input enough threads,
+// four blocks an SM (4 x 4096 x 2048, bf16, backward: 64 us with 128 tokens, 73
+// with 64).
 int conv_run(int B, int L, int C) {
     int run = conv::kLongRun;
-    const auto blocks = [&](int r) { return (double)B * ((L + r * conv::kWarps - 1) / (r * conv::kWarps)) * ((C + 63) / 64); };
+    const auto blocks = [&](int r) { return (double)B * conv_tiles(L, r) * ((C + 63) / 64); };
     while (run > conv::kShortRun && blocks(run) < 4.0 * num_sms()) run /= 2;
     return run;
 }
 
-int conv_tiles(int L, int run) {
-    const int n = run * conv::kWarps;
-    return L > 0 ? (L + n - 1) / n : 1;
+// The forward pass stands on the SMs in waves of four blocks each (eight of
+// single channels), so of the runs the one whose waves are shortest, each with
+// its start counted as eight tokens: 4 x 4096 x 2048, bf16, 576 blocks with runs
+// of 120 29.5 us, 512 with 128 30.1, two waves with 112 35.7 and with 64 32.5.
+int conv_fwd_run(int B, int L, int cols, bool vec) {
+    const double wave = (vec ? 4.0 : 8.0) * num_sms();
+    int best = conv::kLongRun;
+    double least = 1e300;
+    for (int r = conv::kLongRun; r >= conv::kShortRun; r -= conv::kAhead) {
+        const double cost = std::ceil((double)B * conv_tiles(L, r) * cols / wave) * (r + conv::kAhead);
+        if (cost < least) least = cost, best = r;
+    }
+    return best;
 }
 
 efla_status_t check_conv(efla_dtype_t dtype, long long ldx, int B, int L, int C, int K, int heads) {
@@ -393,11 +410,12 @@ efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, co
     conv::Args a{};
     a.x = x; a.ldx = ldx; a.w = weight; a.bias = bias; a.state = state; a.lengths = lengths; a.silu = silu;
     a.head = heads ? C / heads : 0;
-    a.B = B; a.L = L; a.C = C; a.run = conv_run(B, L, C); a.tiles = conv_tiles(L, a.run);
-    a.y = y; a.state_out = state_out;
-    const int row = a.head ? a.head : C, VEC = 4;
+    const int row = heads ? C / heads : C, VEC = 4;
     const bool vec = row % VEC == 0 && rows_in_vectors(x, ldx, VEC, e);
-    const dim3 grid((unsigned)(B * a.tiles), (unsigned)((C + 32 * (vec ? VEC : 1) - 1) / (32 * (vec ? VEC : 1))));
+    const int cols = (C + 32 * (vec ? VEC : 1) - 1) / (32 * (vec ? VEC : 1));
+    a.B = B; a.L = L; a.C = C; a.run = conv_fwd_run(B, L, cols, vec); a.tiles = conv_tiles(L, a.run);
+    a.y = y; a.state_out = state_out;
+    const dim3 grid((unsigned)(B * a.tiles), (unsigned)cols);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == EFLA_F32) {
         if (vec) EFLA_CONV_K(conv::conv_fwd_kernel, float, 4, K, grid, 32 * conv::kWarps, a);

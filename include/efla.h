@@ -263,7 +263,9 @@ efla_status_t efla_chunk_fwd_noalloc(const void *q, const void *k, const void *v
  * other pointers are 16-byte aligned and dense.  `lengths` [B] (int32,
  * device; NULL: all L) is each sequence's number of tokens, taken into
  * [0, L]: tokens from there on are padding, which is not read into any
- * result; their outputs and gradients are zeros.  Outputs must not overlap
+ * result; their outputs and gradients are zeros.  L is at most 0x7fff0000.
+ * Workspaces, as large as the call's _workspace_size says for its sizes, hold
+ * nothing between calls.  Outputs must not overlap
  * inputs or each other, except where a call says so.  Gradients of
  * activations have the activations' dtype, gradients of parameters are fp32.
  * Every sum is taken in fp32 in a fixed order: the same call gives the same
