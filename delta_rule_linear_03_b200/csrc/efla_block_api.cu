@@ -157,15 +157,24 @@ int conv_tiles(int L, int run) {
     return L > 0 ? (L + n - 1) / n : 1;
 }
 
-// Tokens of a thread's run: long ones read fewer rows twice and load their
-// filters less often, short ones give a short or narrow input enough threads,
-// four blocks an SM (4 x 4096 x 2048, bf16, backward: 64 us with 128 tokens, 73
-// with 64).
+// Tokens of a thread's run in the backward pass, a power of two: long runs
+// recompute and add up less (a run costs as much as 18 tokens more), short
+// ones give a short or narrow input enough threads.  The cost of a choice is
+// counted in waves of five blocks an SM, which these times agree with; a part
+// of a wave is bound by latency and takes no less than 0.45 of one.  Odd widths,
+// in single channels, have no runs of 256 (8 x 4096 x 1001, fp32: 104 us, 95
+// with 128).  In us, runs of 16, 32, 64, 128 and 256:
+//   4 x 4096 x 2048, bf16   123  87  73  66  62      1 x 16384 x 1024  66  49  40  37  44
+//   2 x 3000 x 1000, bf16    30  26  22  30  39      32 x 100 x 2048   41  33  38  48  85
 int conv_run(int B, int L, int C) {
-    int run = conv::kLongRun;
-    const auto blocks = [&](int r) { return (double)B * conv_tiles(L, r) * ((C + 63) / 64); };
-    while (run > conv::kShortRun && blocks(run) < 4.0 * num_sms()) run /= 2;
-    return run;
+    int best = conv::kLongRun / 2;
+    double least = 1e300;
+    for (int r = C % 2 ? best : conv::kLongRun; r >= conv::kShortRun; r /= 2) {
+        const double waves = (double)B * conv_tiles(L, r) * ((C + 63) / 64) / (5.0 * num_sms()), part = waves - std::floor(waves);
+        const double cost = (r + 18) * (std::floor(waves) + (part > 0 ? std::max(part, 0.45) : 0.0));
+        if (cost < least) least = cost, best = r;
+    }
+    return best;
 }
 
 // The forward pass stands on the SMs in waves of four blocks each (eight of
@@ -174,9 +183,9 @@ int conv_run(int B, int L, int C) {
 // of 120 29.5 us, 512 with 128 30.1, two waves with 112 35.7 and with 64 32.5.
 int conv_fwd_run(int B, int L, int cols, bool vec) {
     const double wave = (vec ? 4.0 : 8.0) * num_sms();
-    int best = conv::kLongRun;
+    int best = conv::kLongFwdRun;
     double least = 1e300;
-    for (int r = conv::kLongRun; r >= conv::kShortRun; r -= conv::kAhead) {
+    for (int r = conv::kLongFwdRun; r >= conv::kShortRun; r -= conv::kAhead) {
         const double cost = std::ceil((double)B * conv_tiles(L, r) * cols / wave) * (r + conv::kAhead);
         if (cost < least) least = cost, best = r;
     }

@@ -20,7 +20,7 @@
 // block; 32 lanes side by side cover 32 VEC channels.  y may go to
 // [B][H][L][d] directly, the layout the mixer reads.
 //
-// Measured: 4 x 4096 x 2048, bf16, K = 4, 30 us (48 with one channel a thread's
+// Measured: 4 x 4096 x 2048, bf16, K = 4, 29.4 us (48 with one channel a thread's
 // operation, 129 one element at a time); 8 x 2047 x 1001 backward, fp32, odd
 // rows, 36 us (its bytes 30); one token of 64 x 2048 2.1 us, a launch.
 #pragma once
@@ -31,7 +31,7 @@ namespace conv {
 
 constexpr int kWarps = 4;
 constexpr int kAhead = 8;
-constexpr int kShortRun = 16, kLongRun = 128;  // tokens of one thread's run; multiples of kAhead
+constexpr int kShortRun = 8, kLongRun = 256, kLongFwdRun = 128;  // tokens of one thread's run; multiples of kAhead
 
 struct Args {
     const void *x;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
         load_window<T, K, VEC>(a, x, st, t0, len, win);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) d[j] = none<VEC>();
-        const int tl = min(t0 + a.run + K - 1, len);
+        const int tl = min(t0 + a.run + K - 1, len), te = min(t0 + a.run, a.L) + K - 1;  // te: dx is complete
         const T *in = x + t0 * a.ldx, *dy = static_cast<const T *>(a.dy) + out_at(a, b, t0, c);
         T *dx = static_cast<T *>(a.dx) + ((long long)b * a.L + t0 - (K - 1)) * a.C + c;  // of token t - (K-1)
         Raw<T, VEC> nx[U], ny[U];
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
                 win[K - 1 + u] = vals<T, VEC>(nx[u]);
                 d[K - 1 + u] = vals<T, VEC>(ny[u]);
             }
-            if (t + U < t0 + a.run + K - 1) {
+            if (t + U < te) {
                 if (t + 2 * U <= tl) load(t + U, Yes{});
                 else load(t + U, No{});
             }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
             }
         };
         load(t0, No{});
-        for (int t = t0; t < t0 + a.run + K - 1; t += U) {
+        for (int t = t0; t < te; t += U) {
             // the first batch completes tokens before the run, the last those behind it; state_out's rows end at len
             if (t >= t0 + K - 1 && t + U <= t0 + a.run && t + U <= len - (K - 1)) batch(t, Yes{});
             else batch(t, No{});
