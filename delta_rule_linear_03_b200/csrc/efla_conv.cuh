@@ -235,9 +235,11 @@ __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(Args a) {
 // The run of a thread computes d for its own tokens and the K-1 after them,
 // which its last dx need; dw and dbias count its own tokens alone.  The runs
 // of a block add theirs up in shared memory and the block writes one partial
-// row, which colsum_kernel adds in a fixed order.
+// row, which colsum_kernel adds in a fixed order.  Four blocks an SM, five of
+// single channels: with three, of 142 registers, 4 x 4096 x 2048 in fp32 takes 97
+// us, not 72, and with four of single channels 8 x 4096 x 1001 105, not 95.
 template <typename T, int K, int VEC>
-__global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
+__global__ void __launch_bounds__(32 * kWarps, VEC == 1 ? 5 : 4) conv_bwd_kernel(Args a) {
     constexpr int U = kAhead, NE = Vals<VEC>::NE;
     __shared__ float red[kWarps][32 * VEC * (K + 1)];
     const int b = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
         load_window<T, K, VEC>(a, x, st, t0, len, win);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) d[j] = none<VEC>();
-        const int tl = min(t0 + a.run + K - 1, len), te = min(t0 + a.run, a.L) + K - 1;  // te: dx is complete
+        const int tl = min(t0 + a.run + K - 1, len);
         const T *in = x + t0 * a.ldx, *dy = static_cast<const T *>(a.dy) + out_at(a, b, t0, c);
         T *dx = static_cast<T *>(a.dx) + ((long long)b * a.L + t0 - (K - 1)) * a.C + c;  // of token t - (K-1)
         Raw<T, VEC> nx[U], ny[U];
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
                 win[K - 1 + u] = vals<T, VEC>(nx[u]);
                 d[K - 1 + u] = vals<T, VEC>(ny[u]);
             }
-            if (t + U < te) {
+            if (t + U < t0 + a.run + K - 1) {
                 if (t + 2 * U <= tl) load(t + U, Yes{});
                 else load(t + U, No{});
             }
@@ -342,7 +344,8 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(Args a) {
             }
         };
         load(t0, No{});
-        for (int t = t0; t < te; t += U) {
+        for (int t = t0; t < t0 + a.run + K - 1; t += U) {
+            if (t >= a.L + K - 1) break;  // no token's dx is left
             // the first batch completes tokens before the run, the last those behind it; state_out's rows end at len
             if (t >= t0 + K - 1 && t + U <= t0 + a.run && t + U <= len - (K - 1)) batch(t, Yes{});
             else batch(t, No{});
