@@ -288,9 +288,12 @@ efla_status_t check_scan(efla_dtype_t dtype, int B, int L, int C, int G, int N) 
     if ((double)B * (L + 1.0) * C > (double)kMaxElems || (double)B * (L + 1.0) * G * N > (double)kMaxElems ||
         (double)B * C * N > (double)kMaxElems / 64)
         return EFLA_ERR_SHAPE;
-    if (B && C && (double)B * (C + G * 64.0) * (N / 8.0) * 64 > 2147483647.0) return EFLA_ERR_SHAPE;
+    if ((double)C * N > 2147483647.0) return EFLA_ERR_SHAPE;  // a sequence's state values are counted in 32 bits
     return EFLA_OK;
 }
+
+// Whether a grid holds a pass's blocks.
+bool scan_fits(const scan::Plan &p) { return p.blocks * p.nseg <= 0x7fffffffLL; }
 
 template <typename T> efla_status_t run_scan_fwd(const scan::Args &a, const scan::Plan &p, cudaStream_t st) {
     if (p.nseg > 1) {
@@ -522,7 +525,8 @@ efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, v
 
 size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N) {
     if (B <= 0 || L <= 0 || C <= 0 || check_scan(EFLA_F32, B, L, C, G, N) != EFLA_OK) return 0;
-    return seg_floats(scan_plan(B, L, C, G, N, false), B, C, N, false) * sizeof(float);
+    const scan::Plan p = scan_plan(B, L, C, G, N, false);
+    return scan_fits(p) ? seg_floats(p, B, C, N, false) * sizeof(float) : 0;
 }
 
 efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
@@ -545,11 +549,12 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
     }
     if (ldx < C || lddt < C || (z && ldz < C) || ldb < (long long)G * N || ldc < (long long)G * N) return EFLA_ERR_SHAPE;
     if ((double)B * L * std::max({ldx, lddt, z ? ldz : 0, ldb, ldc}) > (double)kMaxElems) return EFLA_ERR_SHAPE;
+    const scan::Plan p = scan_plan(B, L, C, G, N, false);
+    if (!scan_fits(p)) return EFLA_ERR_SHAPE;
     if (!x || !dt || !A || !Bm || !Cm || !y) return EFLA_ERR_NULL;
     if (!aligned_to(x, e) || !aligned_to(dt, e) || !aligned_to(Bm, e) || !aligned_to(Cm, e) || !aligned_to(z, e) ||
         !aligned_to(lengths, 4) || !all_aligned16({A, D, dt_bias, h0, y, h_L, workspace}))
         return EFLA_ERR_ALIGN;
-    const scan::Plan p = scan_plan(B, L, C, G, N, false);
     const size_t need = seg_floats(p, B, C, N, false) * sizeof(float);
     if (need && (!workspace || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
     const long long rows = (long long)B * L;
@@ -571,7 +576,8 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
 
 size_t efla_scan_bwd_workspace_size(int B, int L, int C, int G, int N) {
     if (B <= 0 || L <= 0 || C <= 0 || check_scan(EFLA_F32, B, L, C, G, N) != EFLA_OK) return 0;
-    return bwd_sizes(scan_plan(B, L, C, G, N, true), B, L, C, G, N).bytes();
+    const scan::Plan p = scan_plan(B, L, C, G, N, true);
+    return scan_fits(p) ? bwd_sizes(p, B, L, C, G, N).bytes() : 0;
 }
 
 efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const void *dt, long long lddt,
@@ -601,11 +607,12 @@ efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const 
     }
     if (ldx < C || lddt < C || (z && ldz < C) || ldb < (long long)G * N || ldc < (long long)G * N) return EFLA_ERR_SHAPE;
     if ((double)B * L * std::max({ldx, lddt, z ? ldz : 0, ldb, ldc}) > (double)kMaxElems) return EFLA_ERR_SHAPE;
+    const scan::Plan p = scan_plan(B, L, C, G, N, true);
+    if (!scan_fits(p)) return EFLA_ERR_SHAPE;
     if (!dy || !x || !dt || !A || !Bm || !Cm || !dx || !ddt || !dB || !dC || (z && !dz)) return EFLA_ERR_NULL;
     if (!aligned_to(x, e) || !aligned_to(dt, e) || !aligned_to(Bm, e) || !aligned_to(Cm, e) || !aligned_to(z, e) ||
         !aligned_to(lengths, 4) || !all_aligned16({dy, A, D, dt_bias, h0, dx, ddt, dB, dC, dz, workspace}))
         return EFLA_ERR_ALIGN;
-    const scan::Plan p = scan_plan(B, L, C, G, N, true);
     const BwdSizes z4 = bwd_sizes(p, B, L, C, G, N);
     if (!workspace || workspace_bytes < z4.bytes()) return EFLA_ERR_WORKSPACE;
     const long long rows = (long long)B * L;

@@ -345,7 +345,8 @@ efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, v
  *   A [C][N] fp32, finite; D [C], dt_bias [C] fp32 (or NULL: 0)
  *   h0 [B][C][N] fp32 (NULL: 0); h_L [B][C][N] fp32 (or NULL); h_L may be h0
  *   y [B][L][C]
- * N in {8, 16, 32, 64}; G divides C.
+ * N in {8, 16, 32, 64}; G divides C.  C N is below 2^31, and so are the blocks
+ * of a pass, each of at least 8 channels (or a narrower group) of a sequence.
  */
 size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N);
 efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
