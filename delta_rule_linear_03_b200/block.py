@@ -19,16 +19,34 @@ longer than a one-token step does on the GPU.
 from __future__ import annotations
 
 import ctypes
-import os
 
-import torch  # noqa: F401  (before the extension, which needs its libraries)
+import torch  # before the extension, which needs its libraries
 
 from . import _check, _lib
 
-if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_efla_block.so")):
-    raise ImportError("delta_rule_linear_03_b200/_efla_block.so is missing: build it with "
-                      "`python delta_rule_linear_03_b200/build.py`. There is no fallback implementation.")
-from . import _efla_block as _ext  # noqa: E402
+
+class _Unusable:
+    """Stands for a binding that cannot be loaded: the mixer, which needs none, goes on, and each call of this module says why it fails."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"delta_rule_linear_03_b200/_efla_block.so cannot be used ({self._why}): build it with "
+                          "`python delta_rule_linear_03_b200/build.py`. There is no fallback implementation.")
+
+
+def _load():
+    try:
+        from . import _efla_block as ext
+    except ImportError as e:  # missing, or built against another PyTorch's libraries
+        return _Unusable(e)
+    if ext.torch_version != torch.__version__:  # its C++ interface is one version's
+        return _Unusable(f"it is built for PyTorch {ext.torch_version}, this is {torch.__version__}")
+    return ext
+
+
+_ext = _load()
 
 # The C ABI's own signatures, for callers with raw pointers.
 _p, _i, _l, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t

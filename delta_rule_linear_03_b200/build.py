@@ -6,7 +6,8 @@ side for sm_100a only, and links them with the CUDA runtime, statically, so the
 library needs nothing but the driver at run time.  ``csrc/efla_block_binding.cpp``,
 the Python binding of the operators around the mixer, becomes
 ``_efla_block.so``, against PyTorch's headers and the library.  Rebuilds when
-any source under ``csrc/`` or ``include/`` is newer than either.
+any source under ``csrc/`` or ``include/`` is newer than either; the binding
+also when the installed PyTorch or Python is not the one that it was built for.
 
     python delta_rule_linear_03_b200/build.py [--force]
 
@@ -24,10 +25,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libefla.so")
 BINDING = os.path.join(HERE, "_efla_block.so")
+BUILT_FOR = os.path.join(HERE, "_build", "binding")  # what binding_for() said when the binding was built
 SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu")) +
                  glob.glob(os.path.join(HERE, "csrc", "*.cuh")) +
-                 glob.glob(os.path.join(HERE, "csrc", "*.cpp")) +
                  glob.glob(os.path.join(ROOT, "include", "*.h")))
+BINDING_SOURCE = os.path.join(HERE, "csrc", "efla_block_binding.cpp")
 UNITS = ("efla_api", "efla_block_api", "efla_scan_fwd_f32", "efla_scan_fwd_bf16", "efla_scan_bwd_f32", "efla_scan_bwd_bf16")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
@@ -40,11 +42,30 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def stale() -> bool:
-    if not os.path.exists(SO) or not os.path.exists(BINDING):
+def binding_for() -> str:
+    """The versions whose interfaces the binding is bound to."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def stale_library() -> bool:
+    return not os.path.exists(SO) or any(os.path.getmtime(s) > os.path.getmtime(SO) for s in SOURCES)
+
+
+def stale_binding() -> bool:
+    if not os.path.exists(BINDING) or any(os.path.getmtime(s) > os.path.getmtime(BINDING) for s in (SO, BINDING_SOURCE, *SOURCES)):
         return True
-    t = min(os.path.getmtime(SO), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(s) > t for s in SOURCES)
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read() != binding_for()
+    except OSError:
+        return True
+
+
+def stale() -> bool:
+    return stale_library() or stale_binding()
 
 
 def binding_command(out: str) -> list[str]:
@@ -57,15 +78,23 @@ def binding_command(out: str) -> list[str]:
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_efla_block",
+            f'-DEFLA_TORCH_VERSION="{torch.__version__}"',
             "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
             "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
-            os.path.join(HERE, "csrc", "efla_block_binding.cpp"), "-o", out, "-L" + HERE, "-L" + lib, "-l:libefla.so",
+            BINDING_SOURCE, "-o", out, "-L" + HERE, "-L" + lib, "-l:libefla.so",
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return SO
+    if force or stale_library():
+        build_library(verbose)
+        build_binding()
+    elif stale_binding():
+        build_binding()
+    return SO
+
+
+def build_library(verbose: bool = False) -> None:
     tmp = SO + f".tmp{os.getpid()}"
     objs = [f"{tmp}.{u}.o" for u in UNITS]
     try:
@@ -88,12 +117,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write("".join(said))
     os.replace(tmp, SO)
+
+
+def build_binding() -> None:
     r = subprocess.run(binding_command(BINDING + f".tmp{os.getpid()}"), capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("g++ failed building _efla_block.so")
     os.replace(BINDING + f".tmp{os.getpid()}", BINDING)
-    return SO
+    os.makedirs(os.path.dirname(BUILT_FOR), exist_ok=True)
+    with open(BUILT_FOR, "w") as f:
+        f.write(binding_for())
 
 
 if __name__ == "__main__":

@@ -360,6 +360,7 @@ std::tuple<int, Tensor> scan_step(const Tensor &x, const Tensor &dt, const Tenso
 }  // namespace
 
 PYBIND11_MODULE(_efla_block, m) {
+    m.attr("torch_version") = EFLA_TORCH_VERSION;  // that of the headers and libraries this is built against
     m.def("norm_fwd", &norm_fwd);
     m.def("norm_bwd", &norm_bwd);
     m.def("conv_fwd", &conv_fwd);
