@@ -225,14 +225,20 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {
             Raw<float, VEC> r;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) r.e[j] = a.w[min(max(c + j, 0), C - 1)];
+            // 0 outside the row: an infinite weight at its end would make NaN of the zeros there, and of a scale.  In a
+            // branch of its own, for few vectors: selected at every load, 8190 x 4097 in bf16 to 8 bits takes 147 us, so 110.
+            if (a.y8 && (c < 0 || c + VEC > C))
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    if (c + j < 0 || c + j >= C) r.e[j] = 0.f;
             widen2<float, VEC>(r, w[k]);
         } else {
             widen2<float, VEC>(c < C ? load_raw<float, VEC>(a.w + c) : zero_raw<float, VEC>(), w[k]);
         }
     }
     rs.sum(ss);
-    // columns past C hold zeros, which are no part of a maximum (their product with an infinite
-    // or absent root is kept out)
+    // columns outside the row hold zeros, their weights too, so that they add nothing to a maximum
+    // (the product with an infinite or absent root is kept out where a vector has no column)
     float top[RPI];
 #pragma unroll
     for (int i = 0; i < RPI; ++i) {
