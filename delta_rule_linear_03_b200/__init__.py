@@ -49,7 +49,7 @@ EXPORTS = ("efla_status_string", "efla_version", "efla_last_error", "efla_gate",
            "efla_state_affine", "efla_prefill_bwd_workspace_size", "efla_prefill_bwd",
            "efla_norm_fwd", "efla_norm_bwd_workspace_size", "efla_norm_bwd",
            "efla_conv_fwd", "efla_conv_bwd_workspace_size", "efla_conv_bwd", "efla_conv_step",
-           "efla_scan_fwd_workspace_size", "efla_scan_fwd", "efla_scan_bwd_workspace_size", "efla_scan_bwd",
+           "efla_diag_conv_run", "efla_scan_fwd_workspace_size", "efla_scan_fwd", "efla_scan_bwd_workspace_size", "efla_scan_bwd",
            "efla_scan_step")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 

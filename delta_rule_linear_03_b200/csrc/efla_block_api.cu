@@ -157,21 +157,32 @@ int conv_tiles(int L, int run) {
     return L > 0 ? (L + n - 1) / n : 1;
 }
 
+// Channels of a thread in the backward pass: pairs, where every row of x and
+// of y (whose rows are a head's where there are heads) begins on one.
+int conv_bwd_channels(const void *x, long long ldx, int C, int heads, size_t e) {
+    return (heads ? C / heads : C) % 2 == 0 && rows_in_vectors(x, ldx, 2, e) ? 2 : 1;
+}
+
 // Tokens of a thread's run in the backward pass, a power of two: long runs
-// recompute and add up less (a run costs as much as 18 tokens more), short
-// ones give a short or narrow input enough threads.  The cost of a choice is
-// counted in waves of five blocks an SM, which these times agree with; a part
-// of a wave is bound by latency and takes no less than 0.45 of one.  Odd widths,
-// in single channels, have no runs of 256 (8 x 4096 x 1001, fp32: 104 us, 95
-// with 128).  In us, runs of 16, 32, 64, 128 and 256:
-//   4 x 4096 x 2048, bf16   123  87  73  66  62      1 x 16384 x 1024  66  49  40  37  44
-//   2 x 3000 x 1000, bf16    30  26  22  30  39      32 x 100 x 2048   41  33  38  48  85
-int conv_run(int B, int L, int C) {
-    int best = conv::kLongRun / 2;
+// recompute and add up less, short ones give a short or narrow input enough
+// threads.  The cost of a choice is counted in the waves of its blocks, four an
+// SM of pairs and five of single channels, as their registers allow; a wave
+// takes its runs' tokens and a start of 4 (pairs) or 22 more, and a part of a
+// wave, bound by latency, no less than 0.55 of one.  Of 23 sizes in bf16 and fp32
+// each, this takes the fastest run or one within 1% of it.  Runs of 8, 16, 32, 64,
+// 128 and 256, in us:
+//   pairs    4 x 4096 x 2048, bf16    -   -  86  72  65  61     32 x 100 x 2048, bf16  52  38  28  31  39  39
+//            1 x 16384 x 1024, fp32   -   -  50  45  41  49     18 x 22 x 3584, bf16   19  19  23  23  23  23
+//   singles  8 x 2047 x 1001, fp32    -   -  59  54  57  53     8 x 4096 x 1001, fp32   -   - 110 101  96 105
+//            16 x 1000 x 2050 of odd heads, fp32  -  -  108  98  91  99
+int conv_run(int B, int L, int C, int channels) {
+    const int cols = (C + 32 * channels - 1) / (32 * channels);
+    const double wave = (channels == 2 ? 4.0 : 5.0) * num_sms(), start = channels == 2 ? 4 : 22;
+    int best = conv::kShortRun;
     double least = 1e300;
-    for (int r = C % 2 ? best : conv::kLongRun; r >= conv::kShortRun; r /= 2) {
-        const double waves = (double)B * conv_tiles(L, r) * ((C + 63) / 64) / (5.0 * num_sms()), part = waves - std::floor(waves);
-        const double cost = (r + 18) * (std::floor(waves) + (part > 0 ? std::max(part, 0.45) : 0.0));
+    for (int r = conv::kLongRun; r >= conv::kShortRun; r /= 2) {
+        const double waves = (double)B * conv_tiles(L, r) * cols / wave, part = waves - std::floor(waves);
+        const double cost = (r + start) * (std::floor(waves) + (part > 0 ? std::max(part, 0.55) : 0.0));
         if (cost < least) least = cost, best = r;
     }
     return best;
@@ -441,7 +452,9 @@ efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, co
 
 size_t efla_conv_bwd_workspace_size(int B, int L, int C, int K) {
     if (B <= 0 || L < 0 || L > kMaxLength || C <= 0 || K < 2 || K > 4) return 0;
-    return round16((size_t)B * conv_tiles(L, conv_run(B, L, C)) * C * (K + 1) * sizeof(float));
+    // whichever way the rows turn out to be read
+    const int tiles = std::max(conv_tiles(L, conv_run(B, L, C, 1)), C % 2 ? 0 : conv_tiles(L, conv_run(B, L, C, 2)));
+    return round16((size_t)B * tiles * C * (K + 1) * sizeof(float));
 }
 
 efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_dtype_t dtype, const float *weight,
@@ -474,13 +487,13 @@ efla_status_t efla_conv_bwd(const void *dy, const void *x, long long ldx, efla_d
     conv::Args a{};
     a.x = x; a.ldx = ldx; a.w = weight; a.bias = bias; a.state = state; a.lengths = lengths; a.silu = silu;
     a.head = heads ? C / heads : 0;
-    a.B = B; a.L = L; a.C = C; a.run = conv_run(B, L, C); a.tiles = conv_tiles(L, a.run);
+    const int channels = conv_bwd_channels(x, ldx, C, heads, e);
+    a.B = B; a.L = L; a.C = C; a.run = conv_run(B, L, C, channels); a.tiles = conv_tiles(L, a.run);
     a.dy = dy; a.dstate_out = dstate_out; a.dx = dx; a.dstate = dstate;
     const long long P = (long long)B * a.tiles;
     a.part = static_cast<float *>(workspace);
-    const int row = a.head ? a.head : C;
-    const bool vec = row % 2 == 0 && rows_in_vectors(x, ldx, 2, e);
-    const dim3 grid((unsigned)P, (unsigned)((C + 32 * (vec ? 2 : 1) - 1) / (32 * (vec ? 2 : 1))));
+    const bool vec = channels == 2;
+    const dim3 grid((unsigned)P, (unsigned)((C + 32 * channels - 1) / (32 * channels)));
     if (dtype == EFLA_F32) {
         if (vec) EFLA_CONV_K(conv::conv_bwd_kernel, float, 2, K, grid, 32 * conv::kWarps, a);
         else EFLA_CONV_K(conv::conv_bwd_kernel, float, 1, K, grid, 32 * conv::kWarps, a);
@@ -521,6 +534,11 @@ efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, v
         else EFLA_CONV_K(conv::conv_step_kernel, __nv_bfloat16, 1, K, grid, 128, xp, ldx, sp, weight, bias, yp, silu, C);
     }
     return launched();
+}
+
+int efla_diag_conv_run(int B, int L, int C, int channels, int backward) {
+    if (B <= 0 || L <= 0 || L > kMaxLength || C <= 0 || (channels != 1 && channels != (backward ? 2 : 4))) return 0;
+    return backward ? conv_run(B, L, C, channels) : conv_fwd_run(B, L, (C + 32 * channels - 1) / (32 * channels), channels > 1);
 }
 
 size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N) {

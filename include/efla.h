@@ -337,6 +337,14 @@ efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, v
                              const float *bias, int silu, void *y, int B, int C, int K, efla_stream_t stream);
 
 /*
+ * Diagnostic: tokens of a thread's run in efla_conv_fwd (backward = 0) or
+ * efla_conv_bwd where a thread has `channels` neighbouring channels: forward 4,
+ * backward 2, or 1 where rows or heads are not aligned for that.  0 for other
+ * arguments.  For tests that mean to reach a run of some length.
+ */
+int efla_diag_conv_run(int B, int L, int C, int channels, int backward);
+
+/*
  * efla_scan_fwd - selective state space scan, N state values a channel:
  *     D_t = softplus(dt_t + dt_bias)   (dt_t + dt_bias where `softplus` is 0)
  *     h_t = exp(D_t A) h_{t-1} + D_t x_t B_t,   y_t = (<C_t, h_t> + D x_t) silu(z_t)
