@@ -50,7 +50,7 @@ EXPORTS = ("efla_status_string", "efla_version", "efla_last_error", "efla_gate",
            "efla_norm_fwd", "efla_norm_bwd_workspace_size", "efla_norm_bwd",
            "efla_conv_fwd", "efla_conv_bwd_workspace_size", "efla_conv_bwd", "efla_conv_step",
            "efla_diag_conv_run", "efla_scan_fwd_workspace_size", "efla_scan_fwd", "efla_scan_bwd_workspace_size", "efla_scan_bwd",
-           "efla_scan_step")
+           "efla_diag_scan_plan", "efla_scan_step")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _p, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t

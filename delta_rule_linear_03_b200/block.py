@@ -69,8 +69,9 @@ _lib.efla_scan_bwd_workspace_size.restype = _sz
 _lib.efla_scan_bwd_workspace_size.argtypes = [_i, _i, _i, _i, _i]
 _lib.efla_scan_bwd.argtypes = [_p, _p, _l, _p, _l, _p, _p, _l, _p, _l, _p, _p, _l, _p, _p, _p, _p, _i, _i,
                                _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _sz, _p]
+_lib.efla_diag_scan_plan.argtypes = [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_i)]
 _lib.efla_scan_step.argtypes = [_p, _l, _p, _l, _p, _p, _l, _p, _l, _p, _p, _l, _p, _i, _i, _p, _p, _i, _i, _i, _i, _p]
-for _name in ("norm_fwd", "norm_bwd", "conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step"):
+for _name in ("norm_fwd", "norm_bwd", "conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step", "diag_scan_plan"):
     getattr(_lib, "efla_" + _name).restype = _i
 
 

@@ -547,6 +547,17 @@ size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N) {
     return scan_fits(p) ? seg_floats(p, B, C, N, false) * sizeof(float) : 0;
 }
 
+efla_status_t efla_diag_scan_plan(int B, int L, int C, int G, int N, int backward, int plan[5]) {
+    const efla_status_t s = check_scan(EFLA_F32, B, L, C, G, N);
+    if (s != EFLA_OK) return s;
+    if (!plan) return EFLA_ERR_NULL;
+    if (B == 0 || L == 0 || C == 0) return EFLA_ERR_SHAPE;
+    const scan::Plan p = scan_plan(B, L, C, G, N, backward != 0);
+    if (!scan_fits(p)) return EFLA_ERR_SHAPE;
+    plan[0] = p.ns; plan[1] = p.cp; plan[2] = p.nseg; plan[3] = p.seg; plan[4] = p.tpg;
+    return EFLA_OK;
+}
+
 efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
                             const void *Bm, long long ldb, const void *Cm, long long ldc, const float *D, const void *z,
                             long long ldz, const float *dt_bias, const float *h0, const int *lengths,

@@ -380,6 +380,14 @@ efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const 
                             efla_stream_t stream);
 
 /*
+ * Diagnostic: how efla_scan_fwd (backward = 0) or efla_scan_bwd cuts a call of
+ * these sizes: plan[0] state values of a lane in each of its plan[1] channels,
+ * plan[2] segments of plan[3] tokens, plan[4] channel tiles of a group.  For
+ * tests that mean to reach a variant.
+ */
+efla_status_t efla_diag_scan_plan(int B, int L, int C, int G, int N, int backward, int plan[5]);
+
+/*
  * efla_scan_step - one token: x, dt, z [B][C], Bm, Cm [B][G][N] (rows ld...
  * apart), h [B][C][N] fp32 updated in place, y [B][C].  B <= 65535.
  */
