@@ -60,7 +60,7 @@ _lib.efla_conv_bwd_workspace_size.argtypes = [_i, _i, _i, _i]
 _lib.efla_conv_bwd.argtypes = [_p, _p, _l, _i, _p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _sz, _p]
 _lib.efla_conv_step.argtypes = [_p, _l, _i, _p, _p, _p, _i, _p, _i, _i, _i, _p]
 _lib.efla_diag_conv_run.restype = _i
-_lib.efla_diag_conv_run.argtypes = [_i, _i, _i, _i, _i]
+_lib.efla_diag_conv_run.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.efla_scan_fwd_workspace_size.restype = _sz
 _lib.efla_scan_fwd_workspace_size.argtypes = [_i, _i, _i, _i, _i]
 _lib.efla_scan_fwd.argtypes = [_p, _l, _p, _l, _p, _p, _l, _p, _l, _p, _p, _l, _p, _p, _p, _i, _i, _p, _p,

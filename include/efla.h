@@ -339,10 +339,11 @@ efla_status_t efla_conv_step(const void *x, long long ldx, efla_dtype_t dtype, v
 /*
  * Diagnostic: tokens of a thread's run in efla_conv_fwd (backward = 0) or
  * efla_conv_bwd where a thread has `channels` neighbouring channels: forward 4,
- * backward 2, or 1 where rows or heads are not aligned for that.  0 for other
- * arguments.  For tests that mean to reach a run of some length.
+ * backward 2, or 1 where rows or heads are not aligned for that; lengths: whether
+ * the call has some.  0 for other arguments.  For tests that mean to reach a run
+ * of some length.
  */
-int efla_diag_conv_run(int B, int L, int C, int channels, int backward);
+int efla_diag_conv_run(int B, int L, int C, int channels, int backward, int lengths);
 
 /*
  * efla_scan_fwd - selective state space scan, N state values a channel:

@@ -26,20 +26,22 @@ def _lengths(B, L, r, K):
     return torch.tensor([min(max(at[b % len(at)], 0), L) for b in range(B)], dtype=torch.int32, device="cuda")
 
 
-# batch, length, channels, heads, columns that x begins at in wider rows; channels of a thread and run, backward and forward
-CASES = [(16, 1100, 32, 0, 0, 2, 16, 8), (16, 600, 200, 2, 0, 2, 32, 16), (8, 4100, 130, 0, 0, 2, 64, 40), (16, 4100, 132, 11, 0, 2, 128, 64),
-         (4, 4096, 2048, 16, 0, 2, 256, 120), (1, 4100, 100, 0, 1, 1, 16, 8), (3, 70, 4096, 0, 3, 1, 32, 8), (3, 130, 4095, 0, 0, 1, 64, 16),
-         (3, 260, 4095, 45, 0, 1, 128, 24), (3, 4100, 1000, 8, 0, 1, 256, 88)]
+# batch, length, channels, heads, columns that x begins at in wider rows; channels of a thread; its run backward, without
+# lengths and with, and forward
+CASES = [(16, 1100, 32, 0, 0, 2, 16, 8, 8), (16, 600, 200, 2, 0, 2, 32, 16, 16), (8, 4100, 130, 0, 0, 2, 64, 64, 40), (16, 4100, 132, 11, 0, 2, 128, 128, 64),
+         (4, 4096, 2048, 16, 0, 2, 256, 64, 120), (3, 70, 4096, 0, 3, 1, 32, 16, 8), (3, 130, 4095, 0, 0, 1, 64, 32, 16), (3, 260, 4095, 45, 0, 1, 32, 64, 24),
+         (16, 1000, 2050, 82, 0, 1, 128, 128, 128), (3, 4100, 1000, 8, 0, 1, 256, 128, 88)]
 
 
-@pytest.mark.parametrize("B,L,C,H,off,channels,run,fwd_run", CASES)
+@pytest.mark.parametrize("B,L,C,H,off,channels,whole_run,ragged_run,fwd_run", CASES)
 @pytest.mark.parametrize("K", [2, 3, 4])
 @pytest.mark.parametrize("T", [BF, F])
 @pytest.mark.parametrize("full", [True, False])
-def test_conv_long_runs(efla, B, L, C, H, off, channels, run, fwd_run, K, T, full):
+def test_conv_long_runs(efla, B, L, C, H, off, channels, whole_run, ragged_run, fwd_run, K, T, full):
     diag = efla._lib.efla_diag_conv_run
     wide = channels == 2 and (C // H if H else C) % 4 == 0
-    assert diag(B, L, C, channels, 1) == run and diag(B, L, C, 4 if wide else 1, 0) == fwd_run
+    run = whole_run if full else ragged_run
+    assert diag(B, L, C, channels, 1, 0 if full else 1) == run and diag(B, L, C, 4 if wide else 1, 0, 0) == fwd_run
     g = torch.Generator(device="cuda").manual_seed(L + C + K)
     r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
     x = r(B, L, C + off).to(T)[..., off:]
