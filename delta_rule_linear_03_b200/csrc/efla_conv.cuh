@@ -22,7 +22,8 @@
 //
 // Measured: 4 x 4096 x 2048, bf16, K = 4, 29.7 us (48 with one channel a thread's
 // operation, 129 one element at a time); 8 x 2047 x 1001 backward, fp32, odd
-// rows, 37 us (its bytes 30); one token of 64 x 2048 2.1 us, a launch.
+// rows, random lengths, 38 to 41 us (all its bytes 30); one token of 64 x 2048 2.3
+// us, a launch.
 #pragma once
 #include "efla_vec.cuh"
 

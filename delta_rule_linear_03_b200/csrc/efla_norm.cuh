@@ -17,8 +17,8 @@
 // Measured, of a copy's 6.57 TB/s: 65536 x 2048, bf16 with residual to 8 bits
 // 137 us (all of it; element by element in fp32 it took 272, bound by the ALUs,
 // which now stand at 62%, hence paired operations and conversions); 131008
-// x 128, fp32, 22.4 us (91%); 16384 x 2048 backward, bf16 with an fp32
-// residual, 90.6 us (90%).  64 rows are a launch: 2.4 us.
+// x 128, fp32, 23.2 us (88%); 16384 x 2048 backward, bf16 with an fp32
+// residual, 90.6 us (90%).  64 rows are a launch: 2.7 us.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -166,7 +166,7 @@ __device__ __forceinline__ void store_cols(T *row, int c, int C, bool on, const 
 // vectors begin at the 16-byte boundary before it, and one vector of a group of
 // 128 columns begins in the group before; the groups' maxima meet in shared
 // memory.  Element by element instead, as norm_fwd_any_kernel has it, 33520 x
-// 1001 took 259 us in fp32 (82 with vectors) and 166 in bf16 (95); up to 128
+// 1001 took 259 us in fp32 (82 with vectors) and 166 in bf16 (98); up to 128
 // columns, with two cut vectors in every few, it is the faster (74 against 159).
 template <typename T, typename R, int TPR, int IT, int RPI, bool ANY>
 __global__ void __launch_bounds__(kThreadsOf<TPR>) norm_fwd_kernel(FwdArgs a) {

@@ -27,13 +27,13 @@
 // take longer to read than to exponentiate; with two channels they share B
 // and C, 6 bytes a value.
 //
-// Measured (bf16, gate, N = 16): 4 x 4096 x 2048 forward 268 us, where the 0.54
+// Measured (bf16, gate, N = 16): 4 x 4096 x 2048 forward 269 us, where the 0.54
 // 10^9 exponentials alone take 118 and the preparation's another 30; the special
-// function units are busy 59% of the time, shared memory 64%, on two blocks an
-// SM, which their registers allow.  Four warps that prepare for themselves took
-// 513.  1 x 65536 x 2048, 128 blocks, 1.55 ms: 45 clocks a token of one warp a
-// scheduler, whose loads, exponentials and shuffles go one after another.
-// 8 x 2048 x 1024 backward 545 us.
+// function units are busy 59% of the time, shared memory 64%.  Its 256 blocks
+// leave 40 of the SMs with one where registers allow two.  Four warps that
+// prepare for themselves took 513.  1 x 65536 x 2048, 128 blocks, 1.55 to 1.58
+// ms: 45 clocks a token of one warp a scheduler, whose loads, exponentials and
+// shuffles go one after another.  8 x 2048 x 1024 backward 548 us.
 //
 // Sums over the state index are taken for TB tokens at once: at each halving
 // step a lane sends the half of its values that its partner keeps, so TB sums
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) scan_fwd_kernel(Args a) {
 // clock and SM on two blocks, FMA pipes 41%, special functions 32%, shared
 // memory 53%, while the preparing warps wait for them 40% of their time.
 // Checkpoints every four tokens cost 8 bytes a value of traffic (13% of the copy
-// rate), and every eighth token would need twice the registers.
+// rate); every eighth token would need twice the registers of the recurrence's half.
 
 template <typename S> struct BwdSmem {
     // One order's copy of B or C, so long that the copies which neighbouring lanes read at once lie in
@@ -1044,7 +1044,8 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float *__restrict__ 
 // thread has eight values of a channel's state: with four, the step's
 // softplus and the loads of single values weigh more (256 x 8192 x 16: 61 us
 // against 89, the state's bytes at the copy rate 41), with sixteen, or two
-// sequences, fewer threads are resident (69, 64).  64 x 4096 x 16: 8.4 us.
+// sequences, fewer threads are resident (69, 64).  64 x 4096 x 16: 10.2 to 10.8 us
+// from HBM, 8.0 where L2 holds the states: 4096 blocks in 1.7 waves.
 template <typename T, int N> __global__ void __launch_bounds__(128) scan_step_kernel(Args a) {
     constexpr int NS = 8, LN = N / NS;
     const int i = blockIdx.x * 128 + threadIdx.x, c = i / LN, n0 = (i % LN) * NS, b = blockIdx.y;

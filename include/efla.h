@@ -281,10 +281,14 @@ efla_status_t efla_chunk_fwd_noalloc(const void *q, const void *k, const void *v
  *   y [rows][C] dtype `dtype`, or NULL
  *   y8 [rows][C] e4m3, scale [rows][ceil(C / group)] fp32, or both NULL:
  *     scale = max(max |y| / 448, 2^-126) over each group of columns,
- *     y8 = y / scale rounded to e4m3 (y from the fp32 value, not its rounding)
+ *     y8 = y / scale rounded to e4m3 (y from the fp32 value, not its rounding; the
+ *     quotient in fp32, so that one within 11 2^-24 of the border between two
+ *     values of e4m3 may become either)
  *   group: 128, or 0 for one scale a row.  C <= 16384.
  * At least one of y and y8.  In place: res_out may be res; y or res_out may
- * be x (res_out only where the dtypes agree).
+ * be x (res_out only where the dtypes agree).  Fewer than 2^31 rows.  Squares
+ * are summed in fp32: a row whose mean square passes its range (values from
+ * 10^19 on) is normed to zeros.
  */
 efla_status_t efla_norm_fwd(const void *x, efla_dtype_t dtype, const void *res, efla_dtype_t res_dtype,
                             const float *weight, float eps, void *y, void *y8, float *scale, int group, void *res_out,
@@ -313,6 +317,7 @@ efla_status_t efla_norm_bwd(const void *dy, efla_dtype_t dtype, const void *h, e
  *   state_out [B][K-1][C]: the last K-1 inputs of each sequence (or NULL); may be `state`
  *   y: [B][L][C] where heads is 0, else [B][heads][L][C / heads], the layout
  *     of the mixer's q, k and v
+ * C <= 2097120.
  */
 efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, const float *weight, const float *bias,
                             const void *state, const int *lengths, int silu, void *y, int heads, void *state_out,
@@ -369,7 +374,10 @@ efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long l
  * (NULL: 0): dx, ddt, dz [B][L][C] (dz where there is z), dB, dC
  * [B][L][G][N], all dense in `dtype`; dA [C][N], dD [C] (or NULL), ddt_bias
  * [C] (or NULL), dh0 [B][C][N] (or NULL) fp32.  Nothing of the forward pass
- * is kept for it: the states are recomputed.
+ * is kept for it: the states are recomputed, from checkpoints in the workspace
+ * every few tokens.  With them and the blocks' shares of dB and dC it is large:
+ * some 1.25 N bytes (N = 8 to 32; 1.5 N for 64) for every token and channel, 336
+ * MB for 8 x 2048 x 1024 x 16.
  */
 size_t efla_scan_bwd_workspace_size(int B, int L, int C, int G, int N);
 efla_status_t efla_scan_bwd(const void *dy, const void *x, long long ldx, const void *dt, long long lddt,
