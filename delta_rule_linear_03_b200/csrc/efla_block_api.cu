@@ -15,6 +15,7 @@ using scan::rows_in_vectors;
 namespace {
 
 constexpr int kMaxLength = 0x7fff0000;  // of a sequence: tiles past its end still count in 32 bits
+constexpr long long kMaxBlocks = 0x7fff0000;  // of a grid: colsum_kernel's steps past the last of their rows still count in 32 bits
 
 // One buffer of a call: where it is, how many bytes from its first to its last.
 struct Buf {
@@ -213,7 +214,7 @@ efla_status_t check_conv(efla_dtype_t dtype, long long ldx, int B, int L, int C,
     if (heads && C % heads) return EFLA_ERR_SHAPE;
     if (ldx < C || ldx > kMaxElems) return EFLA_ERR_SHAPE;
     if ((double)B * (L + 4.0) * (double)ldx > (double)kMaxElems) return EFLA_ERR_SHAPE;
-    if ((long long)B * conv_tiles(L, conv::kShortRun) > 0x7fffffffLL || C > 65535 * 32) return EFLA_ERR_SHAPE;
+    if ((long long)B * conv_tiles(L, conv::kShortRun) > kMaxBlocks || C > 65535 * 32) return EFLA_ERR_SHAPE;
     return EFLA_OK;
 }
 
@@ -307,7 +308,7 @@ efla_status_t check_scan(efla_dtype_t dtype, int B, int L, int C, int G, int N) 
 }
 
 // Whether a grid holds a pass's blocks.
-bool scan_fits(const scan::Plan &p) { return p.blocks * p.nseg <= 0x7fffffffLL; }
+bool scan_fits(const scan::Plan &p) { return p.blocks * p.nseg <= kMaxBlocks; }
 
 template <typename T> efla_status_t run_scan_fwd(const scan::Args &a, const scan::Plan &p, cudaStream_t st) {
     if (p.nseg > 1) {

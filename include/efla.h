@@ -317,7 +317,7 @@ efla_status_t efla_norm_bwd(const void *dy, efla_dtype_t dtype, const void *h, e
  *   state_out [B][K-1][C]: the last K-1 inputs of each sequence (or NULL); may be `state`
  *   y: [B][L][C] where heads is 0, else [B][heads][L][C / heads], the layout
  *     of the mixer's q, k and v
- * C <= 2097120.
+ * C <= 2097120, B ceil(L / 32) <= 0x7fff0000.
  */
 efla_status_t efla_conv_fwd(const void *x, long long ldx, efla_dtype_t dtype, const float *weight, const float *bias,
                             const void *state, const int *lengths, int silu, void *y, int heads, void *state_out,
@@ -359,8 +359,9 @@ int efla_diag_conv_run(int B, int L, int C, int channels, int backward, int leng
  *   A [C][N] fp32, finite; D [C], dt_bias [C] fp32 (or NULL: 0)
  *   h0 [B][C][N] fp32 (NULL: 0); h_L [B][C][N] fp32 (or NULL); h_L may be h0
  *   y [B][L][C]
- * N in {8, 16, 32, 64}; G divides C.  C N is below 2^31, and so are the blocks
- * of a pass, each of at least 8 channels (or a narrower group) of a sequence.
+ * N in {8, 16, 32, 64}; G divides C.  C N is below 2^31; the blocks of a pass,
+ * each of at least 8 channels (or a narrower group) of a sequence, are at most
+ * 0x7fff0000.
  */
 size_t efla_scan_fwd_workspace_size(int B, int L, int C, int G, int N);
 efla_status_t efla_scan_fwd(const void *x, long long ldx, const void *dt, long long lddt, const float *A,
